@@ -62,6 +62,7 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_F16 = 2 } pkv_dtype;
 #define PKV_DERR_PAIR 4u     /* a copy pair naming a block outside [0, num_blocks) */
 #define PKV_DERR_CONTEXT 8u  /* context_len < 0 or > max_blocks_per_seq * block_size */
 #define PKV_DERR_TIMEOUT 16u /* a pipeline wait gave up after ~1 s (the call's output is void) */
+#define PKV_DERR_POOL 32u /* kv_resize_requests refused a growth, or the pool's state is not valid */
 
 /*
  * paged_attn_decode -- one decode query token per sequence attends to that sequence's
@@ -307,6 +308,141 @@ int kv_cache_write_fp8(const void* k, const void* v, void* k_cache, void* v_cach
                        const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
                        int head_dim, int block_size, int num_blocks, pkv_dtype dtype,
                        float k_scale, float v_scale, pkv_stream_t stream);
+
+/*
+ * 4-bit caches.
+ *
+ * "PagedAttention: how vLLM manages the KV cache", section "Keep the tensor formula beside
+ * the allocator model": lower-precision cache formats reduce the bytes per element (paging
+ * itself does not).  A row -- the head_dim elements of one token and one KV head -- is held
+ * as head_dim E2M1 codes and one bf16 scale; element d stands for value(code_d) * scale.
+ * E2M1 codes have 1 sign bit, 2 exponent bits (bias 1) and 1 fraction bit: magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6.  They have no NaN and no infinity.
+ *
+ *   k_cache, v_cache    uint8 [num_blocks, block_size, num_kv_heads, head_dim / 2]: element
+ *                       2i of a row in the low four bits of byte i, element 2i + 1 in the
+ *                       high four; 32-byte aligned.
+ *   k_scales, v_scales  bf16 [num_blocks, num_kv_heads, block_size], so that the scales of
+ *                       one block and KV head are contiguous.
+ * head_dim is 32, 64, 128 or 256; block_size is any positive number.  A cached token takes
+ * head_dim + 4 bytes per KV head (keys and values), against 4 * head_dim in a 16-bit cache.
+ * kv_copy_blocks and kv_swap_blocks move blocks of the codes (block_size * num_kv_heads *
+ * head_dim / 2 bytes) and of the scales (block_size * num_kv_heads * 2 bytes) as of any
+ * cache tensor.
+ */
+
+/*
+ * kv_cache_write_fp4 -- kv_cache_write into a 4-bit cache.
+ *
+ * For each row x of token i: scale = the bf16 nearest to amax(|x|) / 6 (the division in IEEE
+ * fp32), and each code the E2M1 value nearest to x_d / scale (IEEE fp32; ties to the even
+ * code; magnitudes beyond 6 saturate).  A scale of zero (amax below bf16's range) gives codes
+ * of zero.  A row that holds a NaN or an infinity gets a NaN scale and codes of zero: every
+ * element of it reads as NaN.  k and v are [num_tokens, num_kv_heads, head_dim] in `dtype`
+ * (any of the three types), 16-byte aligned.  Slot rules and return codes are those of
+ * kv_cache_write (PKV_EUNSUPPORTED for another head_dim); equal inputs give equal codes.
+ */
+int kv_cache_write_fp4(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scales,
+                       void* v_scales, const int64_t* slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * kv_cache_read_fp4 -- read rows of a 4-bit cache back as values.
+ *
+ * k[i] and v[i] become value(code) * scale (the product in fp32, rounded to `dtype`) of the
+ * rows in slot slot_mapping[i], for instance to lay a context out in 16 bits for
+ * paged_attn_prefill: [num_tokens, num_kv_heads, head_dim] with num_tokens a multiple of
+ * block_size is a cache whose block table is 0, 1, 2, ...  Slots may repeat.  Rows with a
+ * negative slot are left as they were; a slot >= num_blocks * block_size too, and it sets
+ * PKV_DERR_SLOT.  k and v are 16-byte aligned.  Return codes as above.
+ */
+int kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache,
+                      const void* k_scales, const void* v_scales, const int64_t* slot_mapping,
+                      int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                      int num_blocks, pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * paged_attn_decode_fp4 -- paged_attn_decode over a 4-bit cache.
+ *
+ *     out[s][h] = sum_p softmax_p( scale * <q[s][h], K_p> ) * V_p
+ * with K_p and V_p the values that the cache's rows stand for.  q and out are [num_seqs,
+ * num_q_heads, head_dim] in `dtype` (any of the three types), 16-byte aligned; softmax
+ * statistics and sums are fp32.  block_tables, context_lens, num_blocks and the device errors
+ * are those of paged_attn_decode: L = 0 gives a zero row, entries and slots past a context are
+ * never used, a live block id out of range sets PKV_DERR_BLOCK_ID and reads as zeros, a
+ * context length outside the table sets PKV_DERR_CONTEXT and is clamped.
+ *
+ * The contexts' 128-token tiles are cut into equal ranges, one CTA for each range and KV head
+ * (and chunk of at most 8 query heads), whatever the lengths of the sequences; a sequence cut
+ * by a range's end is merged by log-sum-exp in a second grid.  The result does not depend on
+ * how the work happened to be scheduled: equal inputs give equal outputs.
+ *
+ *   workspace  device scratch of at least paged_attn_decode_fp4_workspace_size() bytes (may be
+ *              NULL when that is 0), 16-byte aligned; it needs no initialisation, and calls
+ *              that may run concurrently must not share one.
+ * Returns PKV_OK, PKV_EINVAL, PKV_ENOMEM, PKV_EUNSUPPORTED or PKV_ECUDA.
+ */
+size_t paged_attn_decode_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int block_size,
+                                            int max_blocks_per_seq);
+int paged_attn_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                          const void* k_scales, const void* v_scales,
+                          const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype dtype,
+                          void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * kv_resize_requests -- block tables, slot map and free list from request lengths.
+ *
+ * "Why vLLM Uses PagedAttention", section "Split the KV cache into 16-token blocks": a request
+ * holds ceil(tokens / block_size) blocks, named by its block table, which fill left to right.
+ * One call moves every request s from its cached length old_s = context_lens[s] to new_s =
+ * target_lens[s], on the GPU, so that a captured step needs no host work between its steps:
+ *   - growing (a decode token, a prompt chunk, drafted tokens): blocks are taken from the free
+ *     list for logical blocks ceil(old_s / block_size) .. ceil(new_s / block_size) - 1, and the
+ *     slot of each new token (the argument of kv_cache_write) is written to slot_mapping;
+ *   - shrinking (rejected drafts; to 0: a request that finished or is preempted): the blocks
+ *     past ceil(new_s / block_size) go back to the free list.  They must be this request's
+ *     alone; a block that another table names too has to stay out of the list.
+ *
+ * The free list is a ring: block ids free_ring[(head + i) % ring_size], i < count, with head =
+ * pool_state[0] and count = pool_state[1].  Blocks are taken from the head in request order
+ * and returned behind the tail in request order; what a call returns is free from the next
+ * call on.  A ring as long as the pool has blocks never runs over.
+ *
+ * A growth is refused when the new tokens up to and including its own exceed num_rows, or,
+ * if it takes blocks, when the blocks wanted up to and including its own exceed the free
+ * count; wants of refused growths count, so a later request never overtakes an earlier one.
+ * A refused request keeps its length and blocks, its tokens' slots are -1 (kv_cache_write
+ * skips them), and PKV_DERR_POOL is set.
+ *
+ *   block_tables  int32 [num_seqs, max_blocks_per_seq]; entries of taken blocks are written,
+ *                 the others left as they are.
+ *   context_lens  int32 [num_seqs]: old_s on entry, the new lengths on return.
+ *   target_lens   int32 [num_seqs].  A length (old or new) outside [0, max_blocks_per_seq *
+ *                 block_size] leaves the request as it is and sets PKV_DERR_CONTEXT.
+ *   free_ring     int32 [ring_size]; pool_state int32 [4]: head, count and two reserved words.
+ *                 A head outside [0, ring_size) or a count outside [0, ring_size] sets
+ *                 PKV_DERR_POOL and counts as an empty list with head 0.
+ *   slot_mapping  int64 [num_rows] (written; may be NULL when num_rows is 0): token i of
+ *                 request s in row (sum of the growths before s) + i; rows behind the last
+ *                 token are -1.  A block id outside [0, num_blocks) gives -1 and sets
+ *                 PKV_DERR_BLOCK_ID.
+ *   query_start   int32 [num_seqs + 1] (written) or NULL: the first row of each request's
+ *                 tokens and, last, their number (as paged_attn_prefill takes them).
+ *   workspace     device scratch of kv_resize_requests_workspace_size() bytes, 16-byte
+ *                 aligned; it needs no initialisation.
+ * Asynchronous on `stream`; allocates nothing.  Calls on one pool or table must be ordered.
+ * Returns PKV_OK, PKV_EINVAL, PKV_ENOMEM or PKV_ECUDA.
+ */
+size_t kv_resize_requests_workspace_size(int num_seqs);
+int kv_resize_requests(int32_t* block_tables, int32_t* context_lens, const int32_t* target_lens,
+                       int32_t* free_ring, int32_t* pool_state, int64_t* slot_mapping,
+                       int32_t* query_start, int num_seqs, int num_rows, int ring_size,
+                       int block_size, int max_blocks_per_seq, int num_blocks, void* workspace,
+                       size_t workspace_bytes, pkv_stream_t stream);
 
 /*
  * kv_copy_blocks -- copy whole physical blocks of one cache tensor, for copy-on-write.

@@ -23,6 +23,7 @@ PKV_DERR_SLOT = 2
 PKV_DERR_PAIR = 4
 PKV_DERR_CONTEXT = 8
 PKV_DERR_TIMEOUT = 16
+PKV_DERR_POOL = 32
 PKV_ESCRATCH = -5
 PKV_ENODEVMEM = -6
 
@@ -85,6 +86,20 @@ def load() -> ctypes.CDLL:
         lib.kv_cache_write_fp8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, f32, f32,
                                            P]
         lib.kv_cache_write_fp8.restype = i32
+        lib.kv_cache_write_fp4.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P]
+        lib.kv_cache_write_fp4.restype = i32
+        lib.kv_cache_read_fp4.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P]
+        lib.kv_cache_read_fp4.restype = i32
+        lib.paged_attn_decode_fp4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.paged_attn_decode_fp4_workspace_size.restype = sz
+        lib.paged_attn_decode_fp4.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                              i32, i32, f32, i32, P, sz, P]
+        lib.paged_attn_decode_fp4.restype = i32
+        lib.kv_resize_requests_workspace_size.argtypes = [i32]
+        lib.kv_resize_requests_workspace_size.restype = sz
+        lib.kv_resize_requests.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P,
+                                           sz, P]
+        lib.kv_resize_requests.restype = i32
         lib.kv_swap_blocks.argtypes = [P, P, P, i32, sz, i32, i32, P]
         lib.kv_swap_blocks.restype = i32
         lib.pkv_selftest_bounded_wait.argtypes = [ctypes.c_uint, i32, P]
@@ -482,3 +497,183 @@ def kv_cache_write_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                                    _cuda("slot_mapping", slot_mapping), N, Hkv, D, bs, NB,
                                    _dtype(k), float(k_scale), float(v_scale), _stream(stream))
     _check("kv_cache_write_fp8", rc)
+
+
+def _on_current(named) -> None:
+    """The tensors are CUDA tensors, contiguous, of the current device (whose stream the
+    kernels run on)."""
+    here = torch.cuda.current_device()
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.get_device() != here:
+            raise ValueError(f"{name} is on device {t.get_device()}, the current one is {here}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _scratch(device, nbytes: int, workspace, stream) -> torch.Tensor | None:
+    """The caller's workspace, or one of the binding's.
+
+    While a graph is being captured the binding's is a new one, from the graph's own memory
+    pool: the buffer kept for a stream may be replaced by a larger one later, which a
+    replayed graph would not notice, and two graphs must not share one.
+    """
+    if workspace is not None or nbytes == 0:
+        return workspace
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace_for(device, nbytes, stream)
+
+
+def _fp4_shapes(k_cache, v_cache, k_scales, v_scales):
+    """(num_blocks, block_size, num_kv_heads, head_dim) of a 4-bit cache."""
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise TypeError("k_cache and v_cache must hold E2M1 codes as torch.uint8")
+    if k_scales.dtype != torch.bfloat16 or v_scales.dtype != torch.bfloat16:
+        raise TypeError("k_scales and v_scales must be torch.bfloat16")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape [NB, bs, Hkv, D / 2]")
+    NB, bs, Hkv, half = k_cache.shape
+    if tuple(k_scales.shape) != (NB, Hkv, bs) or v_scales.shape != k_scales.shape:
+        raise ValueError("k_scales and v_scales must be [NB, Hkv, bs]")
+    return NB, bs, Hkv, 2 * half
+
+
+def _fp4_rows(fn, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
+    NB, bs, Hkv, D = _fp4_shapes(k_cache, v_cache, k_scales, v_scales)
+    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [N, Hkv, D] matching the cache")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share one element type")
+    N = k.shape[0]
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (N,):
+        raise TypeError("slot_mapping must be int64 [N]")
+    dt = _dtype(k)
+    if N == 0:
+        return
+    _on_current({"k": k, "v": v, "k_cache": k_cache, "v_cache": v_cache, "k_scales": k_scales,
+                 "v_scales": v_scales, "slot_mapping": slot_mapping})
+    rc = getattr(load(), fn)(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), N,
+                             Hkv, D, bs, NB, dt, _stream(stream))
+    _check(fn, rc)
+
+
+def kv_cache_write_fp4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                       slot_mapping: torch.Tensor, stream=None) -> None:
+    """Quantise token rows k[i] / v[i] [N, Hkv, D] into slot slot_mapping[i] of a 4-bit cache.
+
+    ``k_cache`` / ``v_cache`` uint8 [NB, bs, Hkv, D / 2] (two E2M1 codes to a byte, the even
+    element low), ``k_scales`` / ``v_scales`` bf16 [NB, Hkv, bs] (one scale per row).
+    """
+    _fp4_rows("kv_cache_write_fp4", k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+              stream)
+
+
+def kv_cache_read_fp4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                      slot_mapping: torch.Tensor, stream=None) -> None:
+    """Write the values of slot slot_mapping[i] of a 4-bit cache to k[i] / v[i] [N, Hkv, D]."""
+    _fp4_rows("kv_cache_read_fp4", k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+              stream)
+
+
+def paged_attn_decode_fp4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                         head_dim: int, block_size: int,
+                                         max_blocks_per_seq: int) -> int:
+    return int(load().paged_attn_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                           head_dim, block_size,
+                                                           max_blocks_per_seq))
+
+
+def paged_attn_decode_fp4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                          block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Decode over a 4-bit cache (see ``kv_cache_write_fp4``); writes and returns ``out``.
+
+    ``q``/``out`` [B, Hq, D] in fp32, bf16 or fp16; ``block_tables`` int32 [B, MB];
+    ``context_lens`` int32 [B].
+    """
+    NB, bs, Hkv, D = _fp4_shapes(k_cache, v_cache, k_scales, v_scales)
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if q.dtype != out.dtype:
+        raise TypeError("q and out must share one element type")
+    B, Hq, _ = q.shape
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    dt = _dtype(q)
+    lib = load()
+    if B == 0:
+        return out
+    tensors = {"out": out, "q": q, "k_cache": k_cache, "v_cache": v_cache, "k_scales": k_scales,
+               "v_scales": v_scales, "block_tables": block_tables, "context_lens": context_lens}
+    if workspace is not None:
+        tensors["workspace"] = workspace
+    _on_current(tensors)
+    MB = block_tables.shape[1]
+    need = lib.paged_attn_decode_fp4_workspace_size(B, Hq, Hkv, D, bs, MB)
+    workspace = _scratch(q.device, need, workspace, stream)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = lib.paged_attn_decode_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), B, Hq, Hkv, D, bs, MB, NB, float(scale), dt, ws_ptr, ws_bytes,
+        _stream(stream))
+    _check("paged_attn_decode_fp4", rc)
+    return out
+
+
+def kv_resize_requests_workspace_size(num_seqs: int) -> int:
+    return int(load().kv_resize_requests_workspace_size(num_seqs))
+
+
+def kv_resize_requests(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                       target_lens: torch.Tensor, free_ring: torch.Tensor,
+                       pool_state: torch.Tensor, slot_mapping: torch.Tensor,
+                       query_start: torch.Tensor | None, block_size: int, num_blocks: int,
+                       workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Move requests from ``context_lens`` to ``target_lens`` on the GPU (see include/pagedkv.h).
+
+    Updates ``block_tables`` int32 [B, MB], ``context_lens`` int32 [B], the free list
+    (``free_ring`` int32 [R], ``pool_state`` int32 [4]: head, count, two reserved words) and
+    writes ``slot_mapping`` int64 [rows] (-1 behind the last token) and ``query_start`` int32
+    [B + 1].  ``num_blocks`` is the number of blocks of the caches.
+    """
+    ints = {"block_tables": block_tables, "context_lens": context_lens,
+            "target_lens": target_lens, "free_ring": free_ring, "pool_state": pool_state}
+    if query_start is not None:
+        ints["query_start"] = query_start
+    for name, t in ints.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
+        raise TypeError("slot_mapping must be int64 [rows]")
+    if block_tables.dim() != 2 or free_ring.dim() != 1 or tuple(pool_state.shape) != (4,):
+        raise ValueError("block_tables must be [B, MB], free_ring [R] and pool_state [4]")
+    B, MB = block_tables.shape
+    if tuple(context_lens.shape) != (B,) or tuple(target_lens.shape) != (B,):
+        raise ValueError("context_lens and target_lens must be [B]")
+    if query_start is not None and tuple(query_start.shape) != (B + 1,):
+        raise ValueError("query_start must be [B + 1]")
+    lib = load()
+    tensors = dict(ints, slot_mapping=slot_mapping)
+    if workspace is not None:
+        tensors["workspace"] = workspace
+    _on_current(tensors)
+    workspace = _scratch(block_tables.device, lib.kv_resize_requests_workspace_size(B), workspace,
+                         stream)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = lib.kv_resize_requests(
+        block_tables.data_ptr(), context_lens.data_ptr(), target_lens.data_ptr(),
+        free_ring.data_ptr(), pool_state.data_ptr(), slot_mapping.data_ptr(),
+        query_start.data_ptr() if query_start is not None else None, B, slot_mapping.shape[0],
+        free_ring.shape[0], int(block_size), MB, int(num_blocks),
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream))
+    _check("kv_resize_requests", rc)

@@ -353,6 +353,151 @@ int kv_cache_write_fp8(const void* k, const void* v, void* k_cache, void* v_cach
                                    v_scale, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+int cache_fp4(CacheFp4Args& a, bool write, pkv_stream_t stream) {
+  if (a.num_tokens < 0 || a.num_kv_heads <= 0 || a.head_dim <= 0 || a.block_size <= 0 ||
+      a.num_blocks <= 0 || !valid_dtype(a.dtype))
+    return PKV_EINVAL;
+  if (!decode_fp4_supported(a.head_dim, a.block_size)) return PKV_EUNSUPPORTED;
+  if (a.num_tokens == 0) return PKV_OK;
+  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.k_scales || !a.v_scales || !a.slot_mapping)
+    return PKV_EINVAL;
+  if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.k_cache, 16) ||
+      !aligned(a.v_cache, 16) || !aligned(a.k_scales, 2) || !aligned(a.v_scales, 2) ||
+      !aligned(a.slot_mapping, 8))
+    return PKV_EINVAL;
+  a.err = error_word();
+  if (!a.err) return PKV_ECUDA;
+  return launch_cache_fp4(a, write, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+int kv_cache_write_fp4(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scales,
+                       void* v_scales, const int64_t* slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       pkv_dtype dtype, pkv_stream_t stream) {
+  CacheFp4Args a{const_cast<void*>(k), const_cast<void*>(v), k_cache, v_cache, k_scales, v_scales,
+                 slot_mapping, num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype,
+                 nullptr};
+  return cache_fp4(a, true, stream);
+}
+
+int kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache,
+                      const void* k_scales, const void* v_scales, const int64_t* slot_mapping,
+                      int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                      int num_blocks, pkv_dtype dtype, pkv_stream_t stream) {
+  CacheFp4Args a{k, v, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+                 const_cast<void*>(k_scales), const_cast<void*>(v_scales), slot_mapping,
+                 num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype, nullptr};
+  return cache_fp4(a, false, stream);
+}
+
+size_t paged_attn_decode_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int block_size,
+                                            int max_blocks_per_seq) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0)
+    return 0;
+  return decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                   max_blocks_per_seq);
+}
+
+int paged_attn_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                          const void* k_scales, const void* v_scales,
+                          const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype dtype,
+                          void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || !valid_dtype(dtype))
+    return PKV_EINVAL;
+  if (num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+  if (static_cast<long long>(num_blocks) * block_size >= INT_MAX) return PKV_EINVAL;
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= INT_MAX - 128) return PKV_EINVAL;
+  if (!decode_fp4_supported(head_dim, block_size)) return PKV_EUNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables ||
+      !context_lens)
+    return PKV_EINVAL;
+  if (!aligned(k_cache, 32) || !aligned(v_cache, 32) || !aligned(k_scales, 2) ||
+      !aligned(v_scales, 2) || !aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4))
+    return PKV_EINVAL;
+  if (workspace && !aligned(workspace, 16)) return PKV_EINVAL;
+  unsigned* err = error_word();
+  if (!err) return PKV_ECUDA;
+  DecodeFp4Args a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.scale = scale;
+  a.dtype = dtype;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.err = err;
+  return launch_decode_fp4(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kv_resize_requests_workspace_size(int num_seqs) {
+  return num_seqs <= 0 ? 0 : resize_workspace_size(num_seqs);
+}
+
+int kv_resize_requests(int32_t* block_tables, int32_t* context_lens, const int32_t* target_lens,
+                       int32_t* free_ring, int32_t* pool_state, int64_t* slot_mapping,
+                       int32_t* query_start, int num_seqs, int num_rows, int ring_size,
+                       int block_size, int max_blocks_per_seq, int num_blocks, void* workspace,
+                       size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_rows < 0 || ring_size <= 0 || block_size <= 0 ||
+      max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return PKV_EINVAL;
+  // lengths and the sums of blocks taken or given back are 32-bit on the device
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= INT_MAX - block_size ||
+      static_cast<long long>(max_blocks_per_seq) * num_seqs >= INT_MAX)
+    return PKV_EINVAL;
+  if (num_seqs == 0 && num_rows == 0) return PKV_OK;
+  if (num_seqs == 0) return PKV_EINVAL;
+  if (!block_tables || !context_lens || !target_lens || !free_ring || !pool_state ||
+      (num_rows > 0 && !slot_mapping))
+    return PKV_EINVAL;
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(target_lens, 4) ||
+      !aligned(free_ring, 4) || !aligned(pool_state, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(query_start, 4) || !aligned(workspace, 16))
+    return PKV_EINVAL;
+  if (!workspace || workspace_bytes < resize_workspace_size(num_seqs)) return PKV_ENOMEM;
+  ResizeArgs a{};
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.target_lens = target_lens;
+  a.free_ring = free_ring;
+  a.pool_state = pool_state;
+  a.slot_mapping = slot_mapping;
+  a.query_start = query_start;
+  a.num_seqs = num_seqs;
+  a.num_rows = num_rows;
+  a.ring_size = ring_size;
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.workspace = workspace;
+  a.err = error_word();
+  if (!a.err) return PKV_ECUDA;
+  return launch_resize_requests(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int kv_copy_blocks(void* cache, const int64_t* src_dst_pairs, int num_pairs, size_t block_bytes,
                    int num_blocks, pkv_stream_t stream) {
   if (num_pairs < 0 || num_blocks <= 0 || block_bytes == 0) return PKV_EINVAL;
@@ -410,6 +555,8 @@ const char* pkv_strerror(int code) {
     case static_cast<int>(PKV_DERR_SLOT): return "device: slot out of range";
     case static_cast<int>(PKV_DERR_PAIR): return "device: copy pair id out of range";
     case static_cast<int>(PKV_DERR_CONTEXT): return "device: context length outside the block table";
+    case static_cast<int>(PKV_DERR_POOL):
+      return "device: a request's growth refused, or the block pool's state is not valid";
     case static_cast<int>(PKV_DERR_TIMEOUT): return "device: pipeline wait timed out";
     default: return "unknown code";
   }

@@ -1,0 +1,499 @@
+// decode_fp4.cu -- paged single-token decode attention over 4-bit caches (sm_103a).
+//
+// Per cached token and KV head the cache holds two rows (key, value) of head_dim E2M1 codes
+// and one bf16 scale each: head_dim + 4 bytes.  Element d of a key is code_d * ks, so
+//     score(p) = scale * <q, K_p> = (scale * ks_p) * <q, codes(K_p)>,
+//     out      = sum_p softmax(score)_p * vs_p * codes(V_p),
+// and both scales stay outside the products over the codes.
+//
+// Work split.  A sequence of L tokens has ceil(L / 128) tiles.  The tiles of all sequences,
+// in order, are cut into R ranges of equal length (to one tile), and one CTA runs one range
+// for one (KV head, chunk of query heads) unit; the units of a range are neighbouring CTAs,
+// so the heads of one token, which lie side by side in memory, are read together.  A range
+// may begin inside one sequence and end inside another: a CTA leaves (m, l, o) partials for
+// those two, writes the rows of every sequence that lies inside its range itself, and a
+// second grid merges the partials by log-sum-exp.  Equal ranges keep every CTA busy to the
+// end whatever the lengths are, and there are at most 2 partials per CTA.
+#include <algorithm>
+#include <climits>
+
+#include "device_common.cuh"
+#include "fp4.cuh"
+#include "internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kTile = 128;       // tokens of a tile
+constexpr int kHeads = 8;        // query heads of a unit, at most
+constexpr int kRangeCtas = 456;  // CTAs the ranges aim for: three on each of 152 SMs
+constexpr int kSimtWarps = 4;
+constexpr int kSimtThreads = 32 * kSimtWarps;
+
+struct Fp4Params {
+  void* out;
+  const void* q;
+  const uint8_t *k_cache, *v_cache;
+  const __nv_bfloat16 *k_scales, *v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* part_o;    // [ranges][2][num_q_heads][head_dim]
+  float2* part_ml;  // [ranges][2][num_q_heads]: (m in log2 units, l)
+  int2* info;       // [ranges]: the sequence that begins in the range and goes on past it
+                    // (or -1), and the last range that holds tiles of it
+  unsigned* err;
+  int num_seqs, num_q_heads, num_kv_heads, group, chunk, num_chunks;
+  int max_blocks_per_seq, num_blocks, block_size, ranges;
+  float scale_log2;
+};
+
+// Where a range begins: `tiles` tiles from tile `tile` of sequence `s` on; `total` and
+// `begin` are the tiles of the whole batch and those before the range.  Of P.ranges ranges
+// the first `ranges` hold tiles (one each at least), the others are empty.
+struct Span {
+  int s, tile, tiles, ranges;
+  long long total, begin;
+};
+
+__device__ __forceinline__ int live_len(const Fp4Params& P, int s) {
+  const int L = P.context_lens[s], cap = P.max_blocks_per_seq * P.block_size;
+  return L < 0 ? 0 : min(L, cap);
+}
+
+__device__ __forceinline__ long long range_begin(long long total, int ranges, int r) {
+  return total * r / ranges;
+}
+
+// Finds range r; called by all THREADS threads (the first ones of the CTA).  `report`: say
+// so where a context length is outside the block table.
+template <int THREADS>
+__device__ Span find_span(const Fp4Params& P, int r, bool report) {
+  constexpr int W = THREADS / 32;
+  __shared__ long long warp_tot[W];
+  __shared__ int found_s, found_tile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cap = P.max_blocks_per_seq * P.block_size;
+  const int per = (P.num_seqs + THREADS - 1) / THREADS;
+  const int s0 = min(P.num_seqs, tid * per), s1 = min(P.num_seqs, s0 + per);
+  long long own = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int L = P.context_lens[s];
+    if (report && (L < 0 || L > cap)) raise_error(P.err, PKV_DERR_CONTEXT);
+    own += (min(max(L, 0), cap) + kTile - 1) / kTile;
+  }
+  long long incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += warp_tot[w];
+    total += warp_tot[w];
+  }
+  Span sp;
+  sp.total = total;
+  sp.ranges = static_cast<int>(min(static_cast<long long>(P.ranges), total));
+  sp.begin = r < sp.ranges ? range_begin(total, sp.ranges, r) : total;
+  sp.tiles =
+      r < sp.ranges ? static_cast<int>(range_begin(total, sp.ranges, r + 1) - sp.begin) : 0;
+  long long at = before + incl - own;
+  if (at <= sp.begin && sp.begin < at + own) {
+    int s = s0;
+    for (;; ++s) {
+      const int t = (live_len(P, s) + kTile - 1) / kTile;
+      if (sp.begin < at + t) break;
+      at += t;
+    }
+    found_s = s;
+    found_tile = static_cast<int>(sp.begin - at);
+  }
+  __syncthreads();
+  sp.s = sp.tiles > 0 ? found_s : 0;
+  sp.tile = sp.tiles > 0 ? found_tile : 0;
+  return sp;
+}
+
+// The part of one sequence that a range holds.
+struct Segment {
+  int s, L, t0, t1;  // tokens [t0, t1) of sequence s, whose context is L
+  bool whole;        // all of the sequence: its rows are written, not left as partials
+  int slot;          // partial slot: 0 = the sequence began before the range, 1 = it goes on
+};
+
+__device__ __forceinline__ Segment next_segment(const Fp4Params& P, int& s, int& tile,
+                                                int& left) {
+  Segment g;
+  int L = live_len(P, s);
+  while (L == 0) L = live_len(P, ++s);  // left > 0: a sequence with tiles follows
+  const int tiles = (L + kTile - 1) / kTile;
+  const int n = min(left, tiles - tile);
+  g.s = s;
+  g.L = L;
+  g.t0 = tile * kTile;
+  g.t1 = min(L, (tile + n) * kTile);
+  g.whole = n == tiles;
+  g.slot = tile > 0 ? 0 : 1;
+  left -= n;
+  tile = 0;
+  ++s;
+  return g;
+}
+
+// The last segment of a range, when its sequence begins in the range and goes on past it:
+// what the merge grid has to know.  Written by one thread of each range.
+__device__ __forceinline__ void write_info(const Fp4Params& P, int r, const Span& sp) {
+  if (P.ranges <= 1) return;
+  int2 info = make_int2(-1, 0);
+  int s = sp.s, tile = sp.tile, left = sp.tiles;
+  long long at = sp.begin;
+  while (left > 0) {
+    const int first = tile;
+    const Segment g = next_segment(P, s, tile, left);
+    const int tiles = (g.L + kTile - 1) / kTile;
+    if (!g.whole && g.slot == 1) {
+      const long long end = at + tiles;  // the sequence's last tile is end - 1
+      info.x = g.s;
+      info.y = static_cast<int>((end * sp.ranges + sp.total - 1) / sp.total) - 1;
+    }
+    at += tiles - first;
+  }
+  P.info[r] = info;
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_empty_rows(const Fp4Params& P, int D, int r, int h0, int hc,
+                                                int tid, int threads) {
+  for (int s = r; s < P.num_seqs; s += P.ranges) {
+    if (live_len(P, s) > 0) continue;
+    T* out = static_cast<T*>(P.out) + (static_cast<size_t>(s) * P.num_q_heads + h0) * D;
+    for (int i = tid; i < hc * D; i += threads) out[i] = from_f32<T>(0.f);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// CUDA-core path: any type, head_dim 32, 64, 128 or 256, any block size
+// ------------------------------------------------------------------------------------------
+//
+// Warp w takes tokens w, w + 4, ... of a segment; a lane holds head_dim / 32 neighbouring
+// elements of the row and of each query head, and a dot product ends in a warp sum.
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int E>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int lane, float (&x)[E]) {
+  uint32_t w;
+  if constexpr (E == 1)
+    w = __ldg(row + (lane >> 1)) >> (4 * (lane & 1));
+  else if constexpr (E == 2)
+    w = __ldg(row + lane);
+  else if constexpr (E == 4)
+    w = __ldg(reinterpret_cast<const uint16_t*>(row) + lane);
+  else
+    w = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
+  float all[8];
+  decode8(w, 1.f, all);
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = all[e];
+}
+
+template <typename T, int E>
+__global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4Params P) {
+  constexpr int D = 32 * E;
+  __shared__ float o_s[kSimtWarps][kHeads][D];
+  __shared__ float2 ml_s[kSimtWarps][kHeads];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = P.num_kv_heads * P.num_chunks;
+  const int r = blockIdx.x / units, u = blockIdx.x - r * units;
+  const int g = u / P.num_chunks, c = u - g * P.num_chunks;
+  const int h0 = g * P.group + c * P.chunk, hc = min(P.chunk, P.group - c * P.chunk);
+  const int BS = P.block_size;
+  const Span sp = find_span<kSimtThreads>(P, r, u == 0 && r == 0);
+  if (u == 0 && tid == 0) write_info(P, r, sp);
+  zero_empty_rows<T>(P, D, r, h0, hc, tid, kSimtThreads);
+
+  int s = sp.s, tile = sp.tile, left = sp.tiles;
+  while (left > 0) {
+    const Segment seg = next_segment(P, s, tile, left);
+    float qr[kHeads][E], acc[kHeads][E], m[kHeads], l[kHeads];
+    const T* qs = static_cast<const T*>(P.q) +
+                  (static_cast<size_t>(seg.s) * P.num_q_heads + h0) * D + lane * E;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        qr[h][e] = h < hc ? to_f32(qs[h * D + e]) : 0.f;
+        acc[h][e] = 0.f;
+      }
+    }
+    const int32_t* bt = P.block_tables + static_cast<size_t>(seg.s) * P.max_blocks_per_seq;
+    for (int t = seg.t0 + warp; t < seg.t1; t += kSimtWarps) {
+      const int j = t / BS, off = t - j * BS;
+      const int id = __ldg(&bt[j]);
+      float kf[E], vf[E], ks = 0.f, vs = 0.f;
+      if (id >= 0 && id < P.num_blocks) {
+        const size_t row = (static_cast<size_t>(id) * BS + off) * P.num_kv_heads + g;
+        const size_t at = (static_cast<size_t>(id) * P.num_kv_heads + g) * BS + off;
+        load_codes<E>(P.k_cache + row * (D / 2), lane, kf);
+        load_codes<E>(P.v_cache + row * (D / 2), lane, vf);
+        ks = __bfloat162float(P.k_scales[at]);
+        vs = __bfloat162float(P.v_scales[at]);
+      } else {  // reads as zeros
+        if (lane == 0) raise_error(P.err, PKV_DERR_BLOCK_ID);
+#pragma unroll
+        for (int e = 0; e < E; ++e) kf[e] = vf[e] = 0.f;
+      }
+      const float f = ks * P.scale_log2;
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        if (h < hc) {
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) dot = fmaf(qr[h][e], kf[e], dot);
+          const float sl = warp_sum(dot) * f;
+          const float mn = fmaxf(m[h], sl);
+          const float a = exp2f(m[h] - mn), p = exp2f(sl - mn);
+          l[h] = l[h] * a + p;
+          const float pv = p * vs;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(pv, vf[e], acc[h][e] * a);
+          m[h] = mn;
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      if (h < hc) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o_s[warp][h][lane * E + e] = acc[h][e];
+        if (lane == 0) ml_s[warp][h] = make_float2(m[h], l[h]);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < hc * D; i += kSimtThreads) {
+      const int h = i / D, d = i - h * D;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kSimtWarps; ++w) M = fmaxf(M, ml_s[w][h].x);
+      float num = 0.f, den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSimtWarps; ++w) {
+        const float2 ml = ml_s[w][h];
+        // a warp without a token of the segment has m = -inf, l = 0 and o = 0
+        const float cw = ml.x == -INFINITY && ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+        num = fmaf(cw, o_s[w][h][d], num);
+        den = fmaf(cw, ml.y, den);
+      }
+      const int head = h0 + h;
+      if (seg.whole) {
+        static_cast<T*>(P.out)[(static_cast<size_t>(seg.s) * P.num_q_heads + head) * D + d] =
+            from_f32<T>(num / den);
+      } else {
+        const size_t idx = (static_cast<size_t>(r) * 2 + seg.slot) * P.num_q_heads + head;
+        P.part_o[idx * D + d] = num;
+        if (d == 0) P.part_ml[idx] = make_float2(M, den);
+      }
+    }
+    __syncthreads();  // the merge buffers are read before the next segment writes them
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Merge of the partials of sequences cut by a range's end
+// ------------------------------------------------------------------------------------------
+
+constexpr int kMergeWarps = 4;
+
+// One CTA per (range, query head): if a sequence begins in the range and goes on past it,
+// its partials are slot 1 of this range and slot 0 of every later range up to the last that
+// holds tiles of it.  Warp w takes partials w, w + 4, ...:
+//   M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const Fp4Params P) {
+  constexpr int V = D / 32;
+  __shared__ float red[kMergeWarps];
+  __shared__ float o_s[kMergeWarps][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = blockIdx.x, head = blockIdx.y;
+  griddep_wait();
+  const int2 info = __ldcg(&P.info[r]);
+  if (info.x < 0) return;
+  const int np = info.y - r + 1;
+  auto index = [&](int p) {
+    return (static_cast<size_t>(r + p) * 2 + (p == 0 ? 1 : 0)) * P.num_q_heads + head;
+  };
+  float M = -INFINITY;
+  for (int p = tid; p < np; p += 32 * kMergeWarps) M = fmaxf(M, __ldcg(&P.part_ml[index(p)]).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, red[w]);
+  __syncthreads();
+  float acc[V], den = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int p = warp; p < np; p += kMergeWarps) {
+    const size_t idx = index(p);
+    const float2 ml = __ldcg(&P.part_ml[idx]);
+    const float w = exp2f(ml.x - M);
+    den = fmaf(w, ml.y, den);
+    const float* src = P.part_o + idx * D + lane * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, __ldcg(src + k), acc[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = acc[k];
+  if (lane == 0) red[warp] = den;
+  __syncthreads();
+  den = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) den += red[w];
+  T* out = static_cast<T*>(P.out) + (static_cast<size_t>(info.x) * P.num_q_heads + head) * D;
+  for (int d = tid; d < D; d += 32 * kMergeWarps) {
+    float num = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) num += o_s[w][d];
+    out[d] = from_f32<T>(num / den);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------------
+
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+struct Fp4Layout {
+  int chunk, num_chunks, ranges;
+  size_t o_offset, ml_offset, info_offset, total;
+};
+
+Fp4Layout layout(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                 int max_blocks_per_seq) {
+  Fp4Layout w{};
+  const int group = num_q_heads / num_kv_heads;
+  w.num_chunks = (group + kHeads - 1) / kHeads;
+  w.chunk = (group + w.num_chunks - 1) / w.num_chunks;
+  const long long units = static_cast<long long>(num_kv_heads) * w.num_chunks;
+  const long long tiles =
+      static_cast<long long>(num_seqs) *
+      ((static_cast<long long>(max_blocks_per_seq) * block_size + kTile - 1) / kTile);
+  w.ranges = static_cast<int>(std::max(1LL, std::min(kRangeCtas / units, tiles)));
+  if (w.ranges <= 1) return w;
+  const size_t rows = static_cast<size_t>(w.ranges) * 2 * num_q_heads;
+  w.ml_offset = align_up(rows * head_dim * sizeof(float), 256);
+  w.info_offset = w.ml_offset + align_up(rows * sizeof(float2), 256);
+  w.total = w.info_offset + align_up(w.ranges * sizeof(int2), 256);
+  return w;
+}
+
+using Fp4Fn = void (*)(const Fp4Params);
+
+template <typename T>
+Fp4Fn simt_for(int D) {
+  switch (D) {
+    case 32: return decode_fp4_simt_kernel<T, 1>;
+    case 64: return decode_fp4_simt_kernel<T, 2>;
+    case 128: return decode_fp4_simt_kernel<T, 4>;
+    case 256: return decode_fp4_simt_kernel<T, 8>;
+    default: return nullptr;
+  }
+}
+
+template <typename T>
+Fp4Fn merge_for(int D) {
+  switch (D) {
+    case 32: return merge_fp4_kernel<T, 32>;
+    case 64: return merge_fp4_kernel<T, 64>;
+    case 128: return merge_fp4_kernel<T, 128>;
+    case 256: return merge_fp4_kernel<T, 256>;
+    default: return nullptr;
+  }
+}
+
+}  // namespace
+
+size_t decode_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int max_blocks_per_seq) {
+  return layout(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq)
+      .total;
+}
+
+bool decode_fp4_supported(int head_dim, int block_size) {
+  return (head_dim == 32 || head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+         block_size >= 1;
+}
+
+int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
+  const Fp4Layout w = layout(a.num_seqs, a.num_q_heads, a.num_kv_heads, a.head_dim, a.block_size,
+                             a.max_blocks_per_seq);
+  if (w.total > 0 && (a.workspace == nullptr || a.workspace_bytes < w.total)) return PKV_ENOMEM;
+  Fp4Params P{};
+  P.out = a.out;
+  P.q = a.q;
+  P.k_cache = static_cast<const uint8_t*>(a.k_cache);
+  P.v_cache = static_cast<const uint8_t*>(a.v_cache);
+  P.k_scales = static_cast<const __nv_bfloat16*>(a.k_scales);
+  P.v_scales = static_cast<const __nv_bfloat16*>(a.v_scales);
+  P.block_tables = a.block_tables;
+  P.context_lens = a.context_lens;
+  char* ws = static_cast<char*>(a.workspace);
+  if (w.total > 0) {
+    P.part_o = reinterpret_cast<float*>(ws + w.o_offset);
+    P.part_ml = reinterpret_cast<float2*>(ws + w.ml_offset);
+    P.info = reinterpret_cast<int2*>(ws + w.info_offset);
+  }
+  P.err = a.err;
+  P.num_seqs = a.num_seqs;
+  P.num_q_heads = a.num_q_heads;
+  P.num_kv_heads = a.num_kv_heads;
+  P.group = a.num_q_heads / a.num_kv_heads;
+  P.chunk = w.chunk;
+  P.num_chunks = w.num_chunks;
+  P.max_blocks_per_seq = a.max_blocks_per_seq;
+  P.num_blocks = a.num_blocks;
+  P.block_size = a.block_size;
+  P.ranges = w.ranges;
+  P.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  const long long grid = static_cast<long long>(w.ranges) * a.num_kv_heads * w.num_chunks;
+  if (grid > INT_MAX || (w.ranges > 1 && a.num_q_heads > 65535)) return PKV_EUNSUPPORTED;
+  const Fp4Fn fn = a.dtype == PKV_F32    ? simt_for<float>(a.head_dim)
+                   : a.dtype == PKV_BF16 ? simt_for<__nv_bfloat16>(a.head_dim)
+                                         : simt_for<__half>(a.head_dim);
+  const Fp4Fn merge = a.dtype == PKV_F32    ? merge_for<float>(a.head_dim)
+                      : a.dtype == PKV_BF16 ? merge_for<__nv_bfloat16>(a.head_dim)
+                                            : merge_for<__half>(a.head_dim);
+  if (!fn || !merge) return PKV_EUNSUPPORTED;
+  fn<<<static_cast<unsigned>(grid), kSimtThreads, 0, stream>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ECUDA;
+  if (w.ranges > 1) {
+    // launched behind the decode grid while it still runs; its CTAs wait for that grid's end
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(w.ranges - 1), static_cast<unsigned>(a.num_q_heads));
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, merge, P) != cudaSuccess) return PKV_ECUDA;
+  }
+  return PKV_OK;
+}
+
+}  // namespace pkv

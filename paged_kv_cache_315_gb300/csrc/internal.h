@@ -121,6 +121,50 @@ int launch_kv_cache_write_fp8(const void* k, const void* v, void* k_cache, void*
                               pkv_dtype src_dtype, long long num_rows, float k_scale,
                               float v_scale, unsigned* err, cudaStream_t stream);
 
+// Quantising write into (write = true) or read out of a 4-bit cache.
+struct CacheFp4Args {
+  void *k, *v;  // token rows: read by a write, written by a read
+  void *k_cache, *v_cache, *k_scales, *v_scales;
+  const int64_t* slot_mapping;
+  int num_tokens, num_kv_heads, head_dim, block_size, num_blocks;
+  pkv_dtype dtype;
+  unsigned* err;
+};
+int launch_cache_fp4(const CacheFp4Args& a, bool write, cudaStream_t stream);
+
+struct DecodeFp4Args {
+  void* out;
+  const void *q, *k_cache, *v_cache, *k_scales, *v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int num_seqs, num_q_heads, num_kv_heads, head_dim, block_size;
+  int max_blocks_per_seq, num_blocks;
+  float scale;
+  pkv_dtype dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  unsigned* err;
+};
+size_t decode_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int max_blocks_per_seq);
+bool decode_fp4_supported(int head_dim, int block_size);
+int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream);
+
+struct ResizeArgs {
+  int32_t* block_tables;
+  int32_t* context_lens;
+  const int32_t* target_lens;
+  int32_t* free_ring;
+  int32_t* pool_state;
+  int64_t* slot_mapping;
+  int32_t* query_start;
+  int num_seqs, num_rows, ring_size, block_size, max_blocks_per_seq, num_blocks;
+  void* workspace;
+  unsigned* err;
+};
+size_t resize_workspace_size(int num_seqs);
+int launch_resize_requests(const ResizeArgs& a, cudaStream_t stream);
+
 int launch_kv_cache_write(const void* k, const void* v, void* k_cache, void* v_cache,
                           const int64_t* slot_mapping, int num_tokens, size_t row_bytes,
                           long long num_rows, unsigned* err, cudaStream_t stream);
