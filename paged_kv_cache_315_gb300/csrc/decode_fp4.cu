@@ -16,10 +16,13 @@
 // end whatever the lengths are, and there are at most 2 partials per CTA.
 #include <algorithm>
 #include <climits>
+#include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
+#include "umma.cuh"
 
 namespace pkv {
 namespace {
@@ -64,13 +67,15 @@ __device__ __forceinline__ long long range_begin(long long total, int ranges, in
   return total * r / ranges;
 }
 
-// Finds range r; called by all THREADS threads (the first ones of the CTA).  `report`: say
-// so where a context length is outside the block table.
+// Finds range r; called by all THREADS threads of the CTA.  `notes` (one CTA of each range):
+// say so where a context length is outside the block table, and leave P.info[r], which the
+// merge grid reads: the sequence that begins in the range and goes on past it, if there is one.
 template <int THREADS>
-__device__ Span find_span(const Fp4Params& P, int r, bool report) {
+__device__ Span find_span(const Fp4Params& P, int r, bool notes) {
   constexpr int W = THREADS / 32;
   __shared__ long long warp_tot[W];
   __shared__ int found_s, found_tile;
+  __shared__ int2 cut;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = P.max_blocks_per_seq * P.block_size;
   const int per = (P.num_seqs + THREADS - 1) / THREADS;
@@ -78,7 +83,7 @@ __device__ Span find_span(const Fp4Params& P, int r, bool report) {
   long long own = 0;
   for (int s = s0; s < s1; ++s) {
     const int L = P.context_lens[s];
-    if (report && (L < 0 || L > cap)) raise_error(P.err, PKV_DERR_CONTEXT);
+    if (notes && r == 0 && (L < 0 || L > cap)) raise_error(P.err, PKV_DERR_CONTEXT);
     own += (min(max(L, 0), cap) + kTile - 1) / kTile;
   }
   long long incl = own;
@@ -88,6 +93,7 @@ __device__ Span find_span(const Fp4Params& P, int r, bool report) {
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_tot[warp] = incl;
+  if (tid == 0) cut = make_int2(-1, 0);
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
@@ -101,18 +107,31 @@ __device__ Span find_span(const Fp4Params& P, int r, bool report) {
   sp.begin = r < sp.ranges ? range_begin(total, sp.ranges, r) : total;
   sp.tiles =
       r < sp.ranges ? static_cast<int>(range_begin(total, sp.ranges, r + 1) - sp.begin) : 0;
-  long long at = before + incl - own;
-  if (at <= sp.begin && sp.begin < at + own) {
+  const long long at = before + incl - own, end = sp.begin + sp.tiles;
+  // the sequence that holds tile `x`, one of this thread's, and the first tile of it
+  auto holder = [&](long long x, long long& first, int& tiles) {
     int s = s0;
-    for (;; ++s) {
-      const int t = (live_len(P, s) + kTile - 1) / kTile;
-      if (sp.begin < at + t) break;
-      at += t;
+    for (first = at;; ++s) {
+      tiles = (live_len(P, s) + kTile - 1) / kTile;
+      if (x < first + tiles) return s;
+      first += tiles;
     }
-    found_s = s;
-    found_tile = static_cast<int>(sp.begin - at);
+  };
+  long long first;
+  int tiles;
+  if (at <= sp.begin && sp.begin < at + own) {
+    found_s = holder(sp.begin, first, tiles);
+    found_tile = static_cast<int>(sp.begin - first);
+  }
+  if (notes && sp.tiles > 0 && at < end && end < at + own) {
+    const int s = holder(end, first, tiles);
+    // begins in the range and goes on: its last tile lies in the last range that begins at or
+    // before that tile
+    if (first >= sp.begin && first < end)
+      cut = make_int2(s, static_cast<int>(((first + tiles) * sp.ranges + total - 1) / total) - 1);
   }
   __syncthreads();
+  if (notes && tid == 0 && P.ranges > 1) P.info[r] = cut;
   sp.s = sp.tiles > 0 ? found_s : 0;
   sp.tile = sp.tiles > 0 ? found_tile : 0;
   return sp;
@@ -144,27 +163,6 @@ __device__ __forceinline__ Segment next_segment(const Fp4Params& P, int& s, int&
   return g;
 }
 
-// The last segment of a range, when its sequence begins in the range and goes on past it:
-// what the merge grid has to know.  Written by one thread of each range.
-__device__ __forceinline__ void write_info(const Fp4Params& P, int r, const Span& sp) {
-  if (P.ranges <= 1) return;
-  int2 info = make_int2(-1, 0);
-  int s = sp.s, tile = sp.tile, left = sp.tiles;
-  long long at = sp.begin;
-  while (left > 0) {
-    const int first = tile;
-    const Segment g = next_segment(P, s, tile, left);
-    const int tiles = (g.L + kTile - 1) / kTile;
-    if (!g.whole && g.slot == 1) {
-      const long long end = at + tiles;  // the sequence's last tile is end - 1
-      info.x = g.s;
-      info.y = static_cast<int>((end * sp.ranges + sp.total - 1) / sp.total) - 1;
-    }
-    at += tiles - first;
-  }
-  P.info[r] = info;
-}
-
 template <typename T>
 __device__ __forceinline__ void zero_empty_rows(const Fp4Params& P, int D, int r, int h0, int hc,
                                                 int tid, int threads) {
@@ -175,18 +173,20 @@ __device__ __forceinline__ void zero_empty_rows(const Fp4Params& P, int D, int r
   }
 }
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+#include "decode_fp4_umma.cuh"
+
 // ------------------------------------------------------------------------------------------
 // CUDA-core path: any type, head_dim 32, 64, 128 or 256, any block size
 // ------------------------------------------------------------------------------------------
 //
 // Warp w takes tokens w, w + 4, ... of a segment; a lane holds head_dim / 32 neighbouring
 // elements of the row and of each query head, and a dot product ends in a warp sum.
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 template <int E>
 __device__ __forceinline__ void load_codes(const uint8_t* row, int lane, float (&x)[E]) {
@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4
   const int g = u / P.num_chunks, c = u - g * P.num_chunks;
   const int h0 = g * P.group + c * P.chunk, hc = min(P.chunk, P.group - c * P.chunk);
   const int BS = P.block_size;
-  const Span sp = find_span<kSimtThreads>(P, r, u == 0 && r == 0);
-  if (u == 0 && tid == 0) write_info(P, r, sp);
+  const Span sp = find_span<kSimtThreads>(P, r, u == 0);
   zero_empty_rows<T>(P, D, r, h0, hc, tid, kSimtThreads);
 
   int s = sp.s, tile = sp.tile, left = sp.tiles;
@@ -401,7 +400,64 @@ Fp4Layout layout(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, 
   return w;
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// The codes of a cache as a 2-D tensor of 4-bit elements: x = num_kv_heads * 128, y = slots.
+// A box is one block of one KV head: 128 elements (64 bytes, 128 in shared memory) a row.
+bool make_codes_map(CUtensorMap* map, const void* base, int Hkv, long long slots, int block_size) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(Hkv) * 128, static_cast<cuuint64_t>(slots)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(Hkv) * 64};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(block_size)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 using Fp4Fn = void (*)(const Fp4Params);
+using UmmaFn = void (*)(CUtensorMap, CUtensorMap, Fp4Params);
+
+// The tensor-core kernel of a unit of `chunk` query heads, and its shared memory.
+template <typename T>
+UmmaFn umma_for(int chunk, int& smem) {
+  const int HN = chunk <= 1 ? 1 : chunk <= 2 ? 2 : chunk <= 4 ? 4 : 8;
+  smem = u_smem(u_cols(u_terms<T>(), HN));
+  switch (HN) {
+    case 1: return decode_fp4_umma_kernel<T, 1>;
+    case 2: return decode_fp4_umma_kernel<T, 2>;
+    case 4: return decode_fp4_umma_kernel<T, 4>;
+    default: return decode_fp4_umma_kernel<T, 8>;
+  }
+}
+
+// Whether the tensor-core kernel serves a call: TMA wants rows of whole 128-element boxes, a
+// block of 8 to 128 tokens that divides the tile, and 16-byte aligned scales.
+bool uses_umma(const DecodeFp4Args& a) {
+  return a.dtype != PKV_F32 && a.head_dim == 128 &&
+         (a.block_size == 8 || a.block_size == 16 || a.block_size == 32 || a.block_size == 64 ||
+          a.block_size == 128) &&
+         reinterpret_cast<uintptr_t>(a.k_scales) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(a.v_scales) % 16 == 0;
+}
 
 template <typename T>
 Fp4Fn simt_for(int D) {
@@ -478,7 +534,22 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
                       : a.dtype == PKV_BF16 ? merge_for<__nv_bfloat16>(a.head_dim)
                                             : merge_for<__half>(a.head_dim);
   if (!fn || !merge) return PKV_EUNSUPPORTED;
-  fn<<<static_cast<unsigned>(grid), kSimtThreads, 0, stream>>>(P);
+  if (uses_umma(a)) {
+    CUtensorMap kmap, vmap;
+    const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
+    if (!make_codes_map(&kmap, a.k_cache, a.num_kv_heads, slots, a.block_size) ||
+        !make_codes_map(&vmap, a.v_cache, a.num_kv_heads, slots, a.block_size))
+      return PKV_ECUDA;
+    int smem = 0;
+    const UmmaFn ufn = a.dtype == PKV_BF16 ? umma_for<__nv_bfloat16>(w.chunk, smem)
+                                           : umma_for<__half>(w.chunk, smem);
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(ufn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return PKV_ECUDA;
+    ufn<<<static_cast<unsigned>(grid), kUThreads, smem, stream>>>(kmap, vmap, P);
+  } else {
+    fn<<<static_cast<unsigned>(grid), kSimtThreads, 0, stream>>>(P);
+  }
   if (cudaGetLastError() != cudaSuccess) return PKV_ECUDA;
   if (w.ranges > 1) {
     // launched behind the decode grid while it still runs; its CTAs wait for that grid's end

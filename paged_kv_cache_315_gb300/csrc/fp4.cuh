@@ -40,4 +40,18 @@ __device__ __forceinline__ void decode8(uint32_t codes, float scale, float (&x)[
   }
 }
 
+// Two E4M3 codes (`lo` in the low byte) of fp16 or fp32 pairs: nearest, ties to even,
+// magnitudes beyond 448 saturate, NaN stays NaN.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t pair) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(out) : "r"(pair));
+  return out;
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
+  return out;
+}
+
 }  // namespace pkv
