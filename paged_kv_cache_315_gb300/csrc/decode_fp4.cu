@@ -15,6 +15,7 @@
 // second grid merges the partials by log-sum-exp.  Equal ranges keep every CTA busy to the
 // end whatever the lengths are, and there are at most 2 partials per CTA.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <mutex>
 #include <type_traits>

@@ -30,19 +30,23 @@
 // Codes have no NaN, so rows that no copy wrote (past the context, or of an earlier tile) only
 // need a weight of zero.
 //
-// Roles: warps 0-3 softmax and output, warp 4 loads (K, V and scale tiles, and each sequence's
-// query), warp 5 issues the products.  S, P and O are double buffered, and the products run
-// ahead: S(i + 1) is issued before O(i), so the tensor cores score a tile while the softmax
-// warps work on the one before.  Every buffer is released by a barrier that the releasing
-// product or read implies:
-//   - the K slot of tile i by S(i); the V slot, the P buffer, the scales and the notes by O(i),
-//     which follows P(i), which follows their reading;
-//   - the S buffer by P(i), the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives.
+// Roles: warps 0-3 softmax and output; warp 4 loads (K, V and scale tiles, and each sequence's
+// query), warp 5 issues the products.  K, V, S and O are double buffered, and the products run
+// ahead: S(i + 1) is issued before O(i), so the tensor cores score a tile while the softmax warps
+// work on the one before.  V(i - 1) is loaded behind K(i), so that waiting for a V slot holds up
+// no K.  The small scales and notes have four slots.  Every buffer is released by the barrier of
+// a product, which implies all that came before it:
+//   - the K slot of tile i by S(i); the V slot and the P buffer by O(i);
+//   - the S buffer, the scales and the notes by P(i), which follows their reading; S(i + 2) waits
+//     for P(i), and the scales and notes of tile i + 4 for S(i + 2);
+//   - the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives.
+// HBM's copy bandwidth gives each of three CTAs on an SM 2150 clocks for a tile, and the warps'
+// chains have to stay below that one by one: TMA copies and products are issued by an elected
+// thread in straight-line code (45-60 clocks a copy; by eight lanes side by side 80).
 
-constexpr int kUStages = 2;
 constexpr int kUTileBytes = kTile * 128;  // a K or V tile in shared memory (64 of 128 bytes data)
-constexpr int kUSoftmax = 128;
 constexpr int kUThreads = 192;
+constexpr int kUScaleBytes = 4 * 2 * kTile * 2;  // [4 slots][K, V][128 tokens] bf16
 
 // Terms of a 16-bit number, and the columns of S and O: term * HN + head, padded to an N that
 // the instruction has for M = 128.
@@ -50,22 +54,23 @@ template <typename T>
 constexpr int u_terms() { return std::is_same<T, __half>::value ? 3 : 2; }
 __host__ __device__ constexpr int u_cols(int terms, int HN) { return terms * HN <= 16 ? 16 : 32; }
 __host__ __device__ constexpr int u_smem(int NC) {
-  return 1024 + 4 * kUTileBytes + 2 * NC * 128 + 2 * NC * kTile + 1024 + 704;
+  return 1024 + 4 * kUTileBytes + 2 * NC * 128 + NC * kTile + kUScaleBytes + 1088;
 }
 
 // What the warps tell each other, behind the tiles.
 struct USmem {
-  int4 meta[2];          // per tile slot: flags, sequence, live tokens
-  float f[2][kHeads];    // per tile slot: score factor of each head, 2^-e scale log2(e)
+  int4 meta[4];          // per tile: flags, sequence, live tokens
+  float f[4][kHeads];    // per tile, first of a sequence: score factor of each head
   float top[2][4][kHeads];
   uint32_t vtop[2][4];
   float lsum[4][kHeads];
-  uint64_t bars[16];
+  uint64_t bars[17];
+  int qslot[2];          // per tile: query buffer | first tile of a sequence << 1
+  int4 rows[2][4];       // per tile: the cache row of each block
   uint32_t tmem;
-  int qslot[2];          // per tile slot: query buffer | first tile of a sequence << 1
   volatile int abort;
 };
-static_assert(sizeof(USmem) <= 704, "bookkeeping area");
+static_assert(sizeof(USmem) <= 1088, "bookkeeping area");
 
 enum { kFirst = 1, kLast = 2, kWhole = 4, kSlot1 = 8 };
 
@@ -92,18 +97,96 @@ __device__ __forceinline__ bool softmax_sync_and(bool ok) {
   return r != 0;
 }
 
-// Untiled bulk copy (16-byte aligned addresses and size) with completion on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+// 16 bytes from global to shared memory, and an arrival on `bar` once this thread's copies
+// before it are complete.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The `np` blocks of a tile, `step` bytes apart in shared memory, from the cache rows in `rows`;
+// issued by one thread.
+__device__ __forceinline__ void load_blocks(uint32_t dst, uint32_t step, const CUtensorMap* map,
+                                            uint32_t bar, int x, const int4* rows, int np,
+                                            uint32_t bytes) {
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll 2
+  for (int p = 0; p < np; p += 4, dst += 4 * step) {
+    const int4 y = rows[p >> 2];
+    tma_load_2d(dst, map, bar, x, y.x);
+    if (p + 1 < np) tma_load_2d(dst + step, map, bar, x, y.y);
+    if (p + 2 < np) tma_load_2d(dst + 2 * step, map, bar, x, y.z);
+    if (p + 3 < np) tma_load_2d(dst + 3 * step, map, bar, x, y.w);
+  }
 }
 
 __device__ __forceinline__ float pow2_bits(int field) {
   return __uint_as_float(static_cast<uint32_t>(field) << 23);
+}
+
+// Two fp32 operations in one instruction, on neighbouring heads; H = 1 has no pair.
+template <int H>
+__device__ __forceinline__ void fma_heads(float (&d)[H], const float (&a)[H], const float (&b)[H],
+                                          const float (&c)[H]) {
+  if constexpr (H == 1) {
+    d[0] = fmaf(a[0], b[0], c[0]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < H; h += 2)
+      asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+          "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+          : "=f"(d[h]), "=f"(d[h + 1])
+          : "f"(a[h]), "f"(a[h + 1]), "f"(b[h]), "f"(b[h + 1]), "f"(c[h]), "f"(c[h + 1]));
+  }
+}
+
+template <int H>
+__device__ __forceinline__ void fma_heads(float (&d)[H], const float (&a)[H], float b,
+                                          const float (&c)[H]) {
+  float bb[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) bb[h] = b;
+  fma_heads(d, a, bb, c);
+}
+
+template <int H>
+__device__ __forceinline__ void mul_heads(float (&d)[H], const float (&a)[H], const float (&b)[H]) {
+  if constexpr (H == 1) {
+    d[0] = a[0] * b[0];
+  } else {
+#pragma unroll
+    for (int h = 0; h < H; h += 2)
+      asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+          "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+          : "=f"(d[h]), "=f"(d[h + 1])
+          : "f"(a[h]), "f"(a[h + 1]), "f"(b[h]), "f"(b[h + 1]));
+  }
+}
+
+template <int H>
+__device__ __forceinline__ void mul_heads(float (&d)[H], const float (&a)[H], float b) {
+  float bb[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) bb[h] = b;
+  mul_heads(d, a, bb);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Columns that a row of S or O is read in.
@@ -139,12 +222,16 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
   }
 }
 
-// The sum of a head's terms.
+// The sum of each head's terms.
 template <int NT, int HN>
-__device__ __forceinline__ float join_terms(const uint32_t (&r)[NT * HN], int h) {
-  float v = fmaf(__uint_as_float(r[HN + h]), 0.0625f, __uint_as_float(r[h]));
-  if constexpr (NT == 3) v = fmaf(__uint_as_float(r[2 * HN + h]), 0.00390625f, v);
-  return v;
+__device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], float (&v)[HN]) {
+  float t[NT][HN];
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int h = 0; h < HN; ++h) t[q][h] = __uint_as_float(r[q * HN + h]);
+  fma_heads(v, t[1], 0.0625f, t[0]);
+  if constexpr (NT == 3) fma_heads(v, t[2], 0.00390625f, v);
 }
 
 template <typename T, int HN>
@@ -175,16 +262,19 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   uint8_t* k_tiles = base;
   uint8_t* v_tiles = k_tiles + 2 * kUTileBytes;
   uint8_t* q_rows = v_tiles + 2 * kUTileBytes;        // [2][NC][128], 128-byte swizzle
-  uint8_t* p_rows = q_rows + 2 * NC * 128;            // [2][NC / 16][128 tokens][16]
-  __nv_bfloat16* scales = reinterpret_cast<__nv_bfloat16*>(p_rows + 2 * NC * kTile);
-  USmem& sm = *reinterpret_cast<USmem*>(reinterpret_cast<uint8_t*>(scales) + 1024);
-  // bars: K full, V full, scales full, S full, P full, O full, Q full (two each), drain
+  uint8_t* p_rows = q_rows + 2 * NC * 128;            // [NC / 16][128 tokens][16]
+  __nv_bfloat16* scales = reinterpret_cast<__nv_bfloat16*>(p_rows + NC * kTile);
+  USmem& sm = *reinterpret_cast<USmem*>(reinterpret_cast<uint8_t*>(scales) + kUScaleBytes);
+  // barriers: K, V loaded, S, O complete, P written, Q written (two slots each), scales (four),
+  // drain
+  enum { kK = 0, kV, kS, kP, kO, kQ };
   auto bar = [&](int kind, int slot) { return smem_addr(&sm.bars[2 * kind + slot]); };
-  enum { kK = 0, kV, kSc, kS, kP, kO, kQ, kDrain };
+  auto scale_bar = [&](int i) { return smem_addr(&sm.bars[12 + (i & 3)]); };
+  const uint32_t drain_bar = smem_addr(&sm.bars[16]);
 
   if (tid == 0) {
-    for (int kind = kK; kind <= kDrain; ++kind)
-      for (int b = 0; b < 2; ++b) mbar_init(bar(kind, b), kind == kP ? 4 : 1);
+    for (int k = 0; k < 17; ++k)  // scales: an arrival of each lane, and one for the notes
+      mbar_init(smem_addr(&sm.bars[k]), k / 2 == kP ? 4 : k >= 12 && k < 16 ? 33 : 1);
     sm.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
@@ -207,17 +297,15 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     raise_error(P.err, PKV_DERR_TIMEOUT);
     sm.abort = 1;
   };
-  // one lane's wait for tile i's use of a two-slot barrier, for the whole warp
+  // A whole warp's wait for tile i's use of a two-slot barrier; false after an abort.  Mostly
+  // the phase is complete already.
   auto warp_wait = [&](int kind, int i) -> bool {
-    int ok = 1;
-    if (lane == 0) {
-      ok = mbar_wait_bounded(bar(kind, i & 1), (i >> 1) & 1) ? 1 : 0;
-      if (!ok) fail();
-      if (sm.abort) ok = 0;
-    }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();  // what lane 0 acquired holds for the whole warp
-    return ok != 0;
+    const uint32_t at = bar(kind, i & 1), parity = (i >> 1) & 1;
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(at, parity));
+    if (!ok && lane == 0) fail();
+    __syncwarp();
+    return !__any_sync(0xffffffffu, sm.abort != 0);
   };
 
   if (warp == 4) {
@@ -232,11 +320,28 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       if (s >= lens_at + 32) load_lens(s);
       return __shfl_sync(0xffffffffu, lens, s - lens_at);
     };
-    auto load_id = [&](int s, int tile, int L) {
-      const int j = tile * pages + lane;
-      return lane < pages && j * BS < L
-                 ? __ldg(&P.block_tables[static_cast<size_t>(s) * P.max_blocks_per_seq + j])
+    // Block ids come 32 at a time, one per lane, and one window ahead: under load a row of the
+    // block table takes longer to arrive than a tile takes.
+    struct Window {
+      int s, L, j, id;  // the lane's id is that of logical block j + lane of sequence s
+    };
+    auto load_ids = [&](Window& w) {
+      const int j = w.j + lane;
+      w.id = w.s < P.num_seqs && static_cast<long long>(j) * BS < w.L
+                 ? __ldg(&P.block_tables[static_cast<size_t>(w.s) * P.max_blocks_per_seq + j])
                  : -1;
+    };
+    auto next_window = [&](const Window& w) {
+      Window x = w;
+      if (static_cast<long long>(w.j + 32) * BS < w.L) {
+        x.j += 32;
+      } else {
+        x.j = x.L = 0;
+        while (++x.s < P.num_seqs && (x.L = len_of(x.s)) == 0) {
+        }
+      }
+      load_ids(x);
+      return x;
     };
     uint2 qraw[HN];
     auto load_query = [&](int s) {
@@ -246,37 +351,72 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       for (int h = 0; h < HN; ++h)
         qraw[h] = h < hc ? __ldg(reinterpret_cast<const uint2*>(q + h * D)) : make_uint2(0, 0);
     };
+    // the 16 lanes of K and of V take the scales of 8 tokens each
+    const int chunk_page = 8 * (lane & 15) / BS, chunk_off = 8 * (lane & 15) - chunk_page * BS;
+    const __nv_bfloat16* scale_src =
+        (lane < 16 ? P.k_scales : P.v_scales) + static_cast<size_t>(g) * BS + chunk_off;
+    const uint32_t scale_dst = smem_addr(scales + (lane >> 4) * kTile + 8 * (lane & 15));
+    const size_t scale_block = static_cast<size_t>(P.num_kv_heads) * BS;
     load_lens(sp.s);
-    int s = sp.s, tile = sp.tile, L = len_of(s), first_tile = tile, seg = 0;
+    Window now{sp.s, len_of(sp.s), sp.tile * pages / 32 * 32, -1};
+    load_ids(now);
+    load_query(now.s);
+    Window next = next_window(now);
+    int tile = sp.tile, first_tile = tile, seg = 0, np_before = 0;
     bool first = true;
-    int id = load_id(s, tile, L);
-    load_query(s);
+    const uint32_t step = BS * 128;
+    auto load_v = [&](int j, int np) {  // V(j), np blocks
+      if (elect_one())
+        load_blocks(smem_addr(v_tiles + (j & 1) * kUTileBytes), step, &vmap, bar(kV, j & 1), g * D,
+                    sm.rows[j & 1], np, np * BS * 64);
+      __syncwarp();
+    };
     int i = 0;
     for (; i < n; ++i) {
       const int b = i & 1;
-      const int cs = s, cL = L, ct = tile, cid = id;
-      const bool cfirst = first;
-      const int tiles = (cL + kTile - 1) / kTile;
-      const bool clast = ct + 1 == tiles || i + 1 == n;
-      const int valid = min(kTile, cL - ct * kTile);
-      const int np = (valid + BS - 1) / BS;
-      const bool good = lane < np && cid >= 0 && cid < P.num_blocks;
-      if (lane < np && !good) raise_error(P.err, PKV_DERR_BLOCK_ID);
-      const int y = (good ? cid : P.num_blocks) * BS;  // past the cache: reads zeros
-      // the K slot: S(i - 2) has read it
+      const int valid = min(kTile, now.L - tile * kTile);
+      const int at = tile * pages - now.j;   // of the tile's first block in the window
+      const bool block = lane * BS < valid;  // this lane has a block
+      int id = __shfl_sync(0xffffffffu, now.id, (at + lane) & 31);
+      if (block && static_cast<unsigned>(id) >= static_cast<unsigned>(P.num_blocks)) {
+        raise_error(P.err, PKV_DERR_BLOCK_ID);
+        id = -1;
+      }
+      const int np = __popc(__ballot_sync(0xffffffffu, block));
+      // (an id out of range reads zeros, past the cache's end)
+      if (block) reinterpret_cast<int*>(sm.rows[b])[lane] = (id >= 0 ? id : P.num_blocks) * BS;
+      const int cid = __shfl_sync(0xffffffffu, block ? id : -1, chunk_page);
+      __syncwarp();
+      const bool ends = (tile + 1) * kTile >= now.L;  // the sequence ends with this tile
+      const int flags = (first ? kFirst : 0) | (ends || i + 1 == n ? kLast : 0) |
+                        (first_tile == 0 && ends ? kWhole : 0) | (first_tile == 0 ? kSlot1 : 0);
+      const int4 notes = make_int4(flags, now.s, valid, 0);
       if (i >= 2 && !warp_wait(kS, i - 2)) break;
-      if (lane == 0) {
-        sm.qslot[b] = (seg & 1) | (cfirst ? 2 : 0);
-        mbar_arrive_expect_tx(bar(kK, b), np * BS * 64);
+      if (elect_one()) {
+        sm.qslot[b] = (seg & 1) | (first ? 2 : 0);
+        load_blocks(smem_addr(k_tiles + b * kUTileBytes), step, &kmap, bar(kK, b), g * D,
+                    sm.rows[b], np, np * BS * 64);
+        // S(i - 2) is complete, so P(i - 4) had arrived, and with it the softmax warps had read
+        // the slot of scales and notes
+        if (!first) {
+          sm.meta[i & 3] = notes;
+          mbar_arrive(scale_bar(i));
+        }
       }
       __syncwarp();
-      if (lane < np)
-        tma_load_2d(smem_addr(k_tiles + b * kUTileBytes) + lane * BS * 128, &kmap, bar(kK, b),
-                    g * D, y);
-      float factor[HN];
-      if (cfirst) {
-        // the query rows as E4M3 terms.  The buffer's last reader was a product of the
-        // sequence before the last one, no later than S(i - 2).
+      // scales, by one plain asynchronous copy: TMA takes about as long for 32 bytes as for a
+      // block of codes
+      const uint32_t dst = scale_dst + (i & 3) * (4 * kTile);
+      if (cid >= 0)
+        copy16_async(dst, scale_src + cid * scale_block);
+      else
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+      __syncwarp();
+      copy_async_arrive(scale_bar(i));
+      if (first) {
+        float factor[HN];
+        // the query rows as E4M3 terms.  The buffer's last reader was a product of the sequence
+        // before the last one, no later than S(i - 2).
         uint8_t* rows = q_rows + (seg & 1) * NC * 128;
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
@@ -288,16 +428,18 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
           for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
           top = redux_max(top);
           // |x| 2^(134 - E) < 256 for the exponent field E of the largest; a query that is not
-          // finite becomes NaN
+          // finite becomes NaN, and a scale of zero leaves scores of zero
           const int E = max(8, static_cast<int>(top >> 23));
-          const float up = E == 255 ? __uint_as_float(0x7fffffffu) : pow2_bits(261 - E);
-          factor[h] = P.scale_log2 * pow2_bits(E - 7);
+          float up = P.scale_log2 == 0.f ? 0.f : pow2_bits(261 - E);
+          if (E == 255) up = __uint_as_float(0x7fffffffu);
+          factor[h] = P.scale_log2 == 0.f ? 1.f : fabsf(P.scale_log2) * pow2_bits(E - 7);
+          if (factor[h] < FLT_MIN) factor[h] = FLT_MIN;  // masked scores times it stay -inf
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] *= up;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
+          for (int q = 0; q < NT; ++q) {
             const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]), hi = f32x2_to_e4m3x2(x[2], x[3]);
-            const int row = t * HN + h;
+            const int row = q * HN + h;
             *reinterpret_cast<uint32_t*>(rows + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) +
                                          (lane & 3) * 4) = lo | (hi << 16);
             const uint32_t w0 = e4m3x2_to_f16x2(lo), w1 = e4m3x2_to_f16x2(hi);
@@ -310,113 +452,90 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQ, seg & 1));
-      }
-      // what the next tile needs from global memory, while this one waits for its V slot
-      int flags = (cfirst ? kFirst : 0) | (clast ? kLast : 0) |
-                  (first_tile == 0 && ct + 1 == tiles ? kWhole : 0) |
-                  (first_tile == 0 ? kSlot1 : 0);
-      if (i + 1 < n) {
-        first = ct + 1 == tiles;
-        if (first) {
-          ++s;
-          while ((L = len_of(s)) == 0) ++s;
-          tile = first_tile = 0;
-          ++seg;
-          load_query(s);
-        } else {
-          tile = ct + 1;
-        }
-        id = load_id(s, tile, L);
-      }
-      // the V slot, the scales and the tile's notes: O(i - 2) is complete, and P(i - 2), which
-      // it waited for, came after the softmax warps had read tile i - 2's scales and notes
-      if (i >= 2 && !warp_wait(kO, i - 2)) break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(kV, b), np * BS * 64);
-      __syncwarp();
-      if (lane < np)
-        tma_load_2d(smem_addr(v_tiles + b * kUTileBytes) + lane * BS * 128, &vmap, bar(kV, b),
-                    g * D, y);
-      __nv_bfloat16* sk = scales + b * 2 * kTile + lane * BS;
-      if (lane < np && !good) {
-        for (int e = 0; e < BS; ++e) sk[e] = sk[kTile + e] = __float2bfloat16_rn(0.f);
-        fence_proxy_async_smem();
-      }
-      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good));
-      if (lane == 0) {
-        sm.meta[b] = make_int4(flags, cs, valid, 0);
-        if (cfirst) {
+        if (lane == 0) {
+          mbar_arrive(bar(kQ, seg & 1));
 #pragma unroll
-          for (int h = 0; h < HN; ++h) sm.f[b][h] = factor[h];
+          for (int h = 0; h < HN; ++h) sm.f[i & 3][h] = factor[h];
+          sm.meta[i & 3] = notes;
+          mbar_arrive(scale_bar(i));
         }
-        mbar_arrive_expect_tx(bar(kSc, b), copies * BS * 4);
+        __syncwarp();
       }
-      __syncwarp();
-      if (good) {
-        const size_t at = (static_cast<size_t>(cid) * P.num_kv_heads + g) * BS;
-        bulk_load(smem_addr(sk), P.k_scales + at, BS * 2, bar(kSc, b));
-        bulk_load(smem_addr(sk + kTile), P.v_scales + at, BS * 2, bar(kSc, b));
+      // the next tile, and what it needs from global memory
+      if (i + 1 < n) {
+        first = ends;
+        tile = ends ? 0 : tile + 1;
+        if (ends || tile * pages >= now.j + 32) {
+          now = next;
+          next = next_window(next);
+        }
+        if (ends) {
+          load_query(now.s);
+          first_tile = 0;
+          ++seg;
+        }
       }
+      // V(i - 1), behind K(i)
+      if (i >= 1) {
+        if (i >= 3 && !warp_wait(kO, i - 3)) break;
+        load_v(i - 1, np_before);
+      }
+      np_before = np;
     }
+    const bool last = i == n && (n < 3 || warp_wait(kO, n - 3));
+    if (last) load_v(n - 1, np_before);
     // after a wait that ran out, no copy may be in flight when the CTA ends
-    if (i < n) {
-      if (lane == 0) {
-        for (int j = max(0, i - 2); j <= i; ++j) {
-          if (j < i || j >= 2) mbar_wait_for(bar(kK, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
-          if (j < i) {
-            mbar_wait_for(bar(kV, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
-            mbar_wait_for(bar(kSc, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
-          }
-        }
-      }
-      __syncwarp();
+    if (!last && lane == 0) {
+      for (int j = max(0, i - 4); j <= min(i, n - 1); ++j)
+        mbar_wait_for(scale_bar(j), (j >> 2) & 1, kWaitLimitNs / 8);
+      for (int j = max(0, i - 2); j <= min(i, n - 1); ++j)
+        mbar_wait_for(bar(kK, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
+      for (int j = max(0, i - 3); j < i - 1; ++j)
+        mbar_wait_for(bar(kV, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
     }
+    __syncwarp();
   } else if (warp == 5) {
     // ---- products ---------------------------------------------------------------------------
-    bool ok = true;
-    int issued = 0, seg = -1;
-    for (int j = 0; ok && j <= n; ++j) {
+    const uint64_t dk = smem_desc_sw128(smem_addr(k_tiles), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(v_tiles), 1024, 1024);
+    const uint64_t dq = smem_desc_sw128(smem_addr(q_rows), 16, 1024);
+    const uint64_t dp = smem_desc_plain(smem_addr(p_rows), 128, 128);
+    constexpr uint64_t kSlot = kUTileBytes / 16;
+    int seg = -1, j = 0;
+    for (; j <= n; ++j) {
       const int b = j & 1;
       if (j < n) {
-        // S(j) overwrites S(j - 2), which was read before P(j - 2) arrived; this warp waited
-        // for that arrival when it issued O(j - 2)
-        ok = warp_wait(kK, j);
-        if (!ok) break;
+        // S(j) overwrites S(j - 2), which was read before P(j - 2) arrived; this warp waited for
+        // that arrival when it issued O(j - 2)
+        if (!warp_wait(kK, j)) break;
         const int note = sm.qslot[b];
         if (note & 2) {
           ++seg;
-          ok = warp_wait(kQ, seg);
-          if (!ok) break;
+          if (!warp_wait(kQ, seg)) break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after_sync();
-          const uint64_t dk = smem_desc_sw128(smem_addr(k_tiles + b * kUTileBytes), 16, 1024);
-          const uint64_t dq =
-              smem_desc_sw128(smem_addr(q_rows + (note & 1) * NC * 128), 16, 1024);
+          const uint64_t a = dk + b * kSlot, q = dq + (note & 1) * (NC * 8);
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            umma_f8_ss(tm_s + b * NC, dk + kk * 2, dq + kk * 2, kIdS, kk > 0 ? 1u : 0u);
+            umma_f8_ss(tm_s + b * NC, a + kk * 2, q + kk * 2, kIdS, kk > 0 ? 1u : 0u);
           umma_commit(bar(kS, b));
         }
         __syncwarp();
-        issued = 1;
       }
       if (j > 0) {
         // O(i) overwrites O(i - 2), which was read before P(i) arrived
         const int i = j - 1, bi = i & 1;
-        ok = warp_wait(kP, i) && warp_wait(kV, i);
-        if (!ok) break;
-        if (lane == 0) {
+        if (!warp_wait(kV, i) || !warp_wait(kP, i)) break;
+        if (elect_one()) {
           tc_fence_after_sync();
-          const uint64_t dv = smem_desc_sw128(smem_addr(v_tiles + bi * kUTileBytes), 1024, 1024);
+          const uint64_t a = dv + bi * kSlot;
 #pragma unroll
           for (int half = 0; half < NC / 16; ++half) {
-            const uint64_t dp = smem_desc_plain(
-                smem_addr(p_rows + bi * NC * kTile + half * 16 * kTile), 128, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)
-              umma_f8_ss(tm_o + bi * NC + half * 16, dv + kk * 256, dp + kk * 32, kIdO,
-                         kk > 0 ? 1u : 0u);
+              umma_f8_ss(tm_o + bi * NC + half * 16, a + kk * 256, dp + half * kTile + kk * 32,
+                         kIdO, kk > 0 ? 1u : 0u);
           }
           umma_commit(bar(kO, bi));
         }
@@ -424,58 +543,64 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       }
     }
     // every product is complete before tensor memory is released
-    if (issued && lane == 0) {
-      umma_commit(bar(kDrain, 0));
-      if (!mbar_wait_bounded(bar(kDrain, 0), 0)) fail();
+    if (elect_one()) {
+      umma_commit(drain_bar);
+      if (!mbar_wait_bounded(drain_bar, 0)) fail();
     }
     __syncwarp();
   } else {
     // ---- softmax: token tid of S^T, dimension tid of O^T -----------------------------------
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
     float f[HN], acc[HN], l[HN], m[HN], beta[HN];
+    const float sign = P.scale_log2 < 0.f ? -1.f : 1.f;
     bool ok = true;
     // every lane waits; whether all four warps go on is decided at the barriers below
-    auto wait = [&](int kind, int i) -> bool {
-      const bool got = mbar_wait_bounded(bar(kind, i & 1), (i >> 1) & 1);
+    auto wait_bar = [&](uint32_t at, int parity) -> bool {
+      const bool got = mbar_wait_bounded(at, parity);
       const bool all = __all_sync(0xffffffffu, got);
       if (!all && lane == 0) fail();
       return all;
     };
+    auto wait = [&](int kind, int i) { return wait_bar(bar(kind, i & 1), (i >> 1) & 1); };
     auto add_output = [&](int i) {  // acc += O(i) beta
       uint32_t o[COLS];
+      float v[HN];
       tc_fence_after_sync();
       read_columns<COLS>(tm_o + lane_off + (i & 1) * NC, o);
       tc_fence_before_sync();
-#pragma unroll
-      for (int h = 0; h < HN; ++h) acc[h] = fmaf(join_terms<NT, HN>(o, h), beta[h], acc[h]);
+      join_terms<NT, HN>(o, v);
+      fma_heads(acc, v, beta, acc);
     };
     for (int i = 0; i < n; ++i) {
       const int b = i & 1;
-      ok = ok && wait(kSc, i);
-      const int4 meta = sm.meta[b];
+      ok = ok && wait_bar(scale_bar(i), (i >> 2) & 1);
+      const int4 meta = sm.meta[i & 3];
       const int flags = meta.x;
-      const bool live = tid < meta.z;
-      const float ks = __bfloat162float(scales[b * 2 * kTile + tid]);
-      const float vs = live ? __bfloat162float(scales[b * 2 * kTile + kTile + tid]) : 0.f;
+      const __nv_bfloat16* sc = scales + (i & 3) * 2 * kTile + tid;
+      const float ks = __bfloat162float(sc[0]) * sign;
+      float vs = __bfloat162float(sc[kTile]);
       if (flags & kFirst) {
 #pragma unroll
-        for (int h = 0; h < HN; ++h) f[h] = sm.f[b][h];
+        for (int h = 0; h < HN; ++h) f[h] = sm.f[i & 3][h];
       }
       ok = ok && wait(kS, i);
+      // scores but for the head's factor f >= 0, which the exponent below applies
       float x[HN];
       if (ok) {
         uint32_t sr[COLS];
         tc_fence_after_sync();
         read_columns<COLS>(tm_s + lane_off + b * NC, sr);
         tc_fence_before_sync();
-#pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          const float v = join_terms<NT, HN>(sr, h) * (ks * f[h]);
-          x[h] = live ? v : -INFINITY;
-        }
+        join_terms<NT, HN>(sr, x);
+        mul_heads(x, x, ks);
       } else {
 #pragma unroll
         for (int h = 0; h < HN; ++h) x[h] = 0.f;
+      }
+      if (meta.z < kTile && tid >= meta.z) {  // past the context
+        vs = 0.f;
+#pragma unroll
+        for (int h = 0; h < HN; ++h) x[h] = -INFINITY;
       }
       // the tile's largest score of each head and largest |V scale|
       {
@@ -491,16 +616,16 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       }
       ok = softmax_sync_and(ok);
       if (!ok) break;
-      float t[HN];
+      float t[HN], nt[HN], d[HN];
 #pragma unroll
       for (int h = 0; h < HN; ++h)
-        t[h] = fmaxf(fmaxf(sm.top[b][0][h], sm.top[b][1][h]),
-                     fmaxf(sm.top[b][2][h], sm.top[b][3][h]));
+        t[h] = fmaxf(max3(sm.top[b][0][h], sm.top[b][1][h], sm.top[b][2][h]), sm.top[b][3][h]);
       const uint32_t tv = max(max(sm.vtop[b][0], sm.vtop[b][1]), max(sm.vtop[b][2], sm.vtop[b][3]));
       // |vs| 2^(134 - E) < 256 for the exponent field E of the largest
       const int E = min(254, max(8, static_cast<int>(tv >> 23)));
       const float cv = tv >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : vs * pow2_bits(261 - E);
       const float back = pow2_bits(E - 7);
+      mul_heads(t, t, f);  // in log2 units
       if (flags & kFirst) {
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
@@ -508,31 +633,36 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
           acc[h] = 0.f;
           l[h] = 0.f;
         }
-      } else {
-        bool up = false;
+      }
+      fma_heads(d, m, -1.f, t);
+      float most = d[0];
 #pragma unroll
-        for (int h = 0; h < HN; ++h) up = up || t[h] > m[h] + 64.f;
-        if (up) {
+      for (int h = 1; h < HN; ++h) most = fmaxf(most, d[h]);
+      if (most > 64.f) {  // the running reference moves
 #pragma unroll
-          for (int h = 0; h < HN; ++h) {
-            const float mn = fmaxf(m[h], t[h]);
-            const float a = fast_exp2(m[h] - mn);
-            acc[h] *= a;
-            l[h] *= a;
-            beta[h] *= a;
-            m[h] = mn;
-          }
+        for (int h = 0; h < HN; ++h) {
+          const float mn = fmaxf(m[h], t[h]);
+          const float a = fast_exp2(m[h] - mn);
+          acc[h] *= a;
+          l[h] *= a;
+          beta[h] *= a;
+          m[h] = mn;
+          d[h] = t[h] - mn;
         }
       }
-      float w[HN], bh[HN];
+      float w[HN];
+      mul_heads(nt, t, -1.f);
+      fma_heads(x, x, f, nt);
 #pragma unroll
       for (int h = 0; h < HN; ++h) {
-        bh[h] = fast_exp2(t[h] - m[h]);
-        const float p = fast_exp2(x[h] - t[h]);
-        l[h] = fmaf(p, bh[h], l[h]);
-        w[h] = p * cv;
+        d[h] = fast_exp2(d[h]);  // from the tile's reference to the running one
+        x[h] = fast_exp2(x[h]);
       }
-      // the weights' E4M3 terms: byte term * HN + head of the token's row
+      fma_heads(l, x, d, l);
+      mul_heads(w, x, cv);
+      // the weights' E4M3 terms: byte term * HN + head of the token's row.  O(i - 1) has read
+      // the buffer (at a sequence's first tile it was waited for with the last output).
+      if (!(flags & kFirst)) ok = wait(kO, i - 1);
       {
         uint32_t row[NC / 4];
 #pragma unroll
@@ -559,7 +689,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         }
 #pragma unroll
         for (int half = 0; half < NC / 16; ++half)
-          *reinterpret_cast<uint4*>(p_rows + b * NC * kTile + half * 16 * kTile + tid * 16) =
+          *reinterpret_cast<uint4*>(p_rows + half * 16 * kTile + tid * 16) =
               make_uint4(row[4 * half], row[4 * half + 1], row[4 * half + 2], row[4 * half + 3]);
       }
       fence_proxy_async_smem();
@@ -568,12 +698,8 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       if (lane == 0) mbar_arrive(bar(kP, b));
       // the output of the tile before, of the same sequence, while the tensor cores work on
       // this one's; it is read before P(i + 1) arrives, which lets O(i + 1) overwrite it
-      if (!(flags & kFirst)) {
-        ok = wait(kO, i - 1);
-        if (ok) add_output(i - 1);
-      }
-#pragma unroll
-      for (int h = 0; h < HN; ++h) beta[h] = bh[h] * back;
+      if (!(flags & kFirst) && ok) add_output(i - 1);
+      mul_heads(beta, d, back);
       if (flags & kLast) {
         ok = ok && wait(kO, i);
         if (ok) add_output(i);
