@@ -112,7 +112,7 @@ __device__ Span find_span(const Fp4Params& P, int r, bool notes) {
   // the sequence that holds tile `x`, one of this thread's, and the first tile of it
   auto holder = [&](long long x, long long& first, int& tiles) {
     int s = s0;
-    for (first = at;; ++s) {
+    for (first = at;; ++s) {  // one of them holds it
       tiles = (live_len(P, s) + kTile - 1) / kTile;
       if (x < first + tiles) return s;
       first += tiles;

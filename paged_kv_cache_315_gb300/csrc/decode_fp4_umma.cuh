@@ -30,22 +30,27 @@
 // Codes have no NaN, so rows that no copy wrote (past the context, or of an earlier tile) only
 // need a weight of zero.
 //
-// Roles: warps 0-3 softmax and output; warp 4 loads (K, V and scale tiles, and each sequence's
-// query), warp 5 issues the products.  K, V, S and O are double buffered, and the products run
-// ahead: S(i + 1) is issued before O(i), so the tensor cores score a tile while the softmax warps
-// work on the one before.  V(i - 1) is loaded behind K(i), so that waiting for a V slot holds up
-// no K.  The small scales and notes have four slots.  Every buffer is released by the barrier of
-// a product, which implies all that came before it:
-//   - the K slot of tile i by S(i); the V slot and the P buffer by O(i);
-//   - the S buffer, the scales and the notes by P(i), which follows their reading; S(i + 2) waits
-//     for P(i), and the scales and notes of tile i + 4 for S(i + 2);
-//   - the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives.
+// Roles: warps 0-3 softmax and output, warp 4 loads K tiles, warp 5 issues the products, warp 6
+// loads V tiles, warp 7 scales, notes and each sequence's query; the last four walk the range's
+// tiles each for itself.  K, V, S and O are double buffered, and the products run ahead: S(i + 1)
+// is issued before O(i), so the tensor cores score a tile while the softmax warps work on the one
+// before.  The small scales and notes have four slots.  Buffers are released like this:
+//   - the K slot of tile i by S(i), the V slot and the P buffer by O(i);
+//   - the S buffer by P(i), which follows its reading; S(i + 2) waits for it;
+//   - the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives;
+//   - scales and notes by a barrier of their own, a query buffer by the P of the last tile that
+//     used it.
+// A wait by parity must not be lapped: a warp may wait for a barrier's use by tile i only while
+// the use by the next tile of that slot cannot complete without the warp itself (K(i + 2) is what
+// S(i + 2) waits for, V(i + 2) what O(i + 2) does, scales(i + 2) what P(i + 2) does).
 // HBM's copy bandwidth gives each of three CTAs on an SM 2150 clocks for a tile, and the warps'
-// chains have to stay below that one by one: TMA copies and products are issued by an elected
-// thread in straight-line code (45-60 clocks a copy; by eight lanes side by side 80).
+// chains have to stay below that one by one.  With all loads in one warp that warp was the bound
+// (16 TMA copies of a 16-token block each, at 45-60 clocks from an elected thread in straight-line
+// code, 80 from eight lanes side by side).  The registers follow the roles: 80 a thread at launch,
+// then 96 for softmax warps and 64 for the others.
 
 constexpr int kUTileBytes = kTile * 128;  // a K or V tile in shared memory (64 of 128 bytes data)
-constexpr int kUThreads = 192;
+constexpr int kUThreads = 256;
 constexpr int kUScaleBytes = 4 * 2 * kTile * 2;  // [4 slots][K, V][128 tokens] bf16
 
 // Terms of a 16-bit number, and the columns of S and O: term * HN + head, padded to an N that
@@ -64,9 +69,8 @@ struct USmem {
   float top[2][4][kHeads];
   uint32_t vtop[2][4];
   float lsum[4][kHeads];
-  uint64_t bars[17];
-  int qslot[2];          // per tile: query buffer | first tile of a sequence << 1
-  int4 rows[2][4];       // per tile: the cache row of each block
+  uint64_t bars[21];
+  int4 rows[2][4];       // of K, of V: the cache row of each block of a tile
   uint32_t tmem;
   volatile int abort;
 };
@@ -234,6 +238,103 @@ __device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], float (
   if constexpr (NT == 3) fma_heads(v, t[2], 0.00390625f, v);
 }
 
+// Registers of a thread from here on, for the four warps of a warpgroup.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The tiles of a range in order, walked by a whole warp.
+struct Walk {
+  int s, L, tile;  // the tile's sequence, its context length, the tile within it
+  bool first;      // the sequence's first tile in this range
+  int lens_at, lens;
+
+  __device__ __forceinline__ int len_of(const Fp4Params& P, int x) {
+    const int lane = threadIdx.x & 31;
+    if (x >= lens_at + 32) {  // 32 lengths at a time, one per lane
+      lens_at = x;
+      lens = x + lane < P.num_seqs ? live_len(P, x + lane) : 0;
+    }
+    return __shfl_sync(0xffffffffu, lens, x - lens_at);
+  }
+  __device__ __forceinline__ void begin(const Fp4Params& P, const Span& sp) {
+    lens_at = sp.s - 32;
+    s = sp.s;
+    L = len_of(P, s);
+    tile = sp.tile;
+    first = true;
+  }
+  // the sequence ends with this tile
+  __device__ __forceinline__ bool ends() const { return (tile + 1) * kTile >= L; }
+  // (not called behind the range's last tile: a sequence with tiles follows)
+  __device__ __forceinline__ void advance(const Fp4Params& P) {
+    first = ends();
+    if (first) {
+      do {
+        L = len_of(P, ++s);
+      } while (L == 0);
+      tile = 0;
+    } else {
+      ++tile;
+    }
+  }
+};
+
+// The block ids of a range's tiles.  They come 32 at a time, one per lane, and one window ahead:
+// under load a row of the block table takes longer to arrive than a tile takes.
+struct Ids {
+  int s, j, id;     // the lane's id is that of logical block j + lane of sequence s
+  int ns, nj, nid;  // the window behind it
+  Walk ahead;       // at the sequence of the window behind
+
+  __device__ __forceinline__ int load(const Fp4Params& P, int seq, int L, int j0) const {
+    const int x = j0 + static_cast<int>(threadIdx.x & 31);
+    return seq < P.num_seqs && static_cast<long long>(x) * P.block_size < L
+               ? __ldg(&P.block_tables[static_cast<size_t>(seq) * P.max_blocks_per_seq + x])
+               : -1;
+  }
+  __device__ __forceinline__ void load_next(const Fp4Params& P) {
+    ns = ahead.s;
+    nj = j + 32;
+    if (static_cast<long long>(nj) * P.block_size >= ahead.L) {
+      nj = 0;
+      ahead.L = 0;
+      while (++ahead.s < P.num_seqs && (ahead.L = ahead.len_of(P, ahead.s)) == 0) {
+      }
+      ns = ahead.s;
+    }
+    nid = load(P, ns, ahead.L, nj);
+  }
+  __device__ __forceinline__ void begin(const Fp4Params& P, const Walk& w, int pages) {
+    ahead = w;
+    s = w.s;
+    j = w.tile * pages / 32 * 32;
+    id = load(P, s, w.L, j);
+    load_next(P);
+  }
+  // This lane's block of the walk's tile, `block` saying whether it has one: its id, or -1 (and
+  // an error) where that is out of range.
+  __device__ __forceinline__ int of(const Fp4Params& P, const Walk& w, int pages, bool block) {
+    if (w.s != s || w.tile * pages >= j + 32) {
+      s = ns;
+      j = nj;
+      id = nid;
+      load_next(P);
+    }
+    int x = __shfl_sync(0xffffffffu, id, (w.tile * pages - j + (threadIdx.x & 31)) & 31);
+    if (block && static_cast<unsigned>(x) >= static_cast<unsigned>(P.num_blocks)) {
+      raise_error(P.err, PKV_DERR_BLOCK_ID);
+      x = -1;
+    }
+    return x;
+  }
+};
+
 template <typename T, int HN>
 __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 : 2)
     decode_fp4_umma_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -245,6 +346,8 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   constexpr uint32_t kIdS = umma_idesc_e2m1_e4m3(kTile, NC, false, false);
   constexpr uint32_t kIdO = umma_idesc_e2m1_e4m3(D, 16, true, true);
   constexpr uint32_t kTmemCols = NC == 16 ? 64 : 128;
+  // 4 (kManyRegs + kFewRegs) registers of 4 warps are what 8 warps have at launch: 80 or 128 each
+  constexpr int kManyRegs = NC == 16 ? 96 : 168, kFewRegs = NC == 16 ? 64 : 88;
   extern __shared__ uint8_t smem_raw[];
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -253,11 +356,6 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   const int g = u / P.num_chunks, c = u - g * P.num_chunks;
   const int h0 = g * P.group + c * P.chunk, hc = min(P.chunk, P.group - c * P.chunk);
   const int BS = P.block_size;
-  const Span sp = find_span<kUThreads>(P, r, u == 0);  // u == 0 also leaves the merge's notes
-  zero_empty_rows<T>(P, D, r, h0, hc, tid, kUThreads);
-  if (sp.tiles == 0) return;
-  const int n = sp.tiles;
-
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* k_tiles = base;
   uint8_t* v_tiles = k_tiles + 2 * kUTileBytes;
@@ -270,11 +368,13 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   enum { kK = 0, kV, kS, kP, kO, kQ };
   auto bar = [&](int kind, int slot) { return smem_addr(&sm.bars[2 * kind + slot]); };
   auto scale_bar = [&](int i) { return smem_addr(&sm.bars[12 + (i & 3)]); };
-  const uint32_t drain_bar = smem_addr(&sm.bars[16]);
+  auto scale_free_bar = [&](int i) { return smem_addr(&sm.bars[16 + (i & 3)]); };
+  const uint32_t drain_bar = smem_addr(&sm.bars[20]);
 
   if (tid == 0) {
-    for (int k = 0; k < 17; ++k)  // scales: an arrival of each lane, and one for the notes
-      mbar_init(smem_addr(&sm.bars[k]), k / 2 == kP ? 4 : k >= 12 && k < 16 ? 33 : 1);
+    for (int k = 0; k < 21; ++k)  // scales: an arrival of each lane, and one for the notes
+      mbar_init(smem_addr(&sm.bars[k]),
+                k / 2 == kP || (k >= 16 && k < 20) ? 4 : k >= 12 && k < 16 ? 33 : 1);
     sm.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
@@ -289,8 +389,10 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     tmem_relinquish();
   }
   tc_fence_before_sync();
-  __syncthreads();
+  // (synchronises all threads; u == 0 also leaves the merge's notes)
+  const Span sp = find_span<kUThreads>(P, r, u == 0);
   tc_fence_after_sync();
+  const int n = sp.tiles;
   const uint32_t tm_s = sm.tmem, tm_o = tm_s + 2 * NC;
 
   auto fail = [&]() {
@@ -299,257 +401,223 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   };
   // A whole warp's wait for tile i's use of a two-slot barrier; false after an abort.  Mostly
   // the phase is complete already.
-  auto warp_wait = [&](int kind, int i) -> bool {
-    const uint32_t at = bar(kind, i & 1), parity = (i >> 1) & 1;
+  auto warp_wait_bar = [&](uint32_t at, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
     const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(at, parity));
     if (!ok && lane == 0) fail();
     __syncwarp();
     return !__any_sync(0xffffffffu, sm.abort != 0);
   };
+  auto warp_wait = [&](int kind, int i) {
+    return warp_wait_bar(bar(kind, i & 1), (i >> 1) & 1);
+  };
 
-  if (warp == 4) {
-    // ---- loads ----------------------------------------------------------------------------
+  if (warp >= 4) {
+    fewer_registers<kFewRegs>();
     const int pages = kTile / BS;
-    int lens_at = sp.s, lens = 0;  // context lengths of 32 sequences, one per lane
-    auto load_lens = [&](int s) {
-      lens_at = s;
-      lens = s + lane < P.num_seqs ? live_len(P, s + lane) : 0;
-    };
-    auto len_of = [&](int s) {
-      if (s >= lens_at + 32) load_lens(s);
-      return __shfl_sync(0xffffffffu, lens, s - lens_at);
-    };
-    // Block ids come 32 at a time, one per lane, and one window ahead: under load a row of the
-    // block table takes longer to arrive than a tile takes.
-    struct Window {
-      int s, L, j, id;  // the lane's id is that of logical block j + lane of sequence s
-    };
-    auto load_ids = [&](Window& w) {
-      const int j = w.j + lane;
-      w.id = w.s < P.num_seqs && static_cast<long long>(j) * BS < w.L
-                 ? __ldg(&P.block_tables[static_cast<size_t>(w.s) * P.max_blocks_per_seq + j])
-                 : -1;
-    };
-    auto next_window = [&](const Window& w) {
-      Window x = w;
-      if (static_cast<long long>(w.j + 32) * BS < w.L) {
-        x.j += 32;
-      } else {
-        x.j = x.L = 0;
-        while (++x.s < P.num_seqs && (x.L = len_of(x.s)) == 0) {
+    Walk w;
+    if (warp == 4 || warp == 6) {
+      // ---- K tiles (warp 4), V tiles (warp 6) ----------------------------------------------
+      const bool is_k = warp == 4;
+      const int kind = is_k ? kK : kV, freed = is_k ? kS : kO;
+      const CUtensorMap* map = is_k ? &kmap : &vmap;
+      const uint32_t tiles = smem_addr(is_k ? k_tiles : v_tiles);
+      int4* rows = sm.rows[is_k ? 0 : 1];
+      Ids ids;
+      int i = 0;
+      if (n > 0) {
+        w.begin(P, sp);
+        ids.begin(P, w, pages);
+      }
+      for (; i < n; ++i) {
+        const int b = i & 1;
+        const int valid = min(kTile, w.L - w.tile * kTile);
+        const bool block = lane * BS < valid;  // this lane has a block
+        const int np = (valid + BS - 1) / BS;
+        const int id = ids.of(P, w, pages, block);
+        // (an id out of range reads zeros, past the cache's end)
+        if (block) reinterpret_cast<int*>(rows)[lane] = (id >= 0 ? id : P.num_blocks) * BS;
+        __syncwarp();
+        if (i >= 2 && !warp_wait(freed, i - 2)) break;
+        if (elect_one())
+          load_blocks(tiles + b * kUTileBytes, BS * 128, map, bar(kind, b), g * D, rows, np,
+                      np * BS * 64);
+        __syncwarp();
+        if (i + 1 < n) w.advance(P);
+      }
+      // after a wait that ran out, no copy may be in flight when the CTA ends
+      if (i < n && lane == 0)
+        for (int j = max(0, i - 2); j < i; ++j)
+          mbar_wait_for(bar(kind, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
+    } else if (warp == 5) {
+      // ---- products -------------------------------------------------------------------------
+      const uint64_t dk = smem_desc_sw128(smem_addr(k_tiles), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_addr(v_tiles), 1024, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_addr(q_rows), 16, 1024);
+      const uint64_t dp = smem_desc_plain(smem_addr(p_rows), 128, 128);
+      constexpr uint64_t kSlot = kUTileBytes / 16;
+      int seg = -1;
+      if (n > 0) w.begin(P, sp);
+      for (int j = 0; n > 0 && j <= n; ++j) {
+        const int b = j & 1;
+        if (j < n) {
+          // S(j) overwrites S(j - 2), which was read before P(j - 2) arrived; this warp waited
+          // for that arrival when it issued O(j - 2)
+          if (!warp_wait(kK, j)) break;
+          if (w.first) {
+            ++seg;
+            if (!warp_wait(kQ, seg)) break;
+          }
+          if (elect_one()) {
+            tc_fence_after_sync();
+            const uint64_t a = dk + b * kSlot, q = dq + (seg & 1) * (NC * 8);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_f8_ss(tm_s + b * NC, a + kk * 2, q + kk * 2, kIdS, kk > 0 ? 1u : 0u);
+            umma_commit(bar(kS, b));
+          }
+          __syncwarp();
+          if (j + 1 < n) w.advance(P);
+        }
+        if (j > 0) {
+          // O(i) overwrites O(i - 2), which was read before P(i) arrived
+          const int i = j - 1, bi = i & 1;
+          if (!warp_wait(kV, i) || !warp_wait(kP, i)) break;
+          if (elect_one()) {
+            tc_fence_after_sync();
+            const uint64_t a = dv + bi * kSlot;
+#pragma unroll
+            for (int half = 0; half < NC / 16; ++half) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 32; ++kk)
+                umma_f8_ss(tm_o + bi * NC + half * 16, a + kk * 256, dp + half * kTile + kk * 32,
+                           kIdO, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(bar(kO, bi));
+          }
+          __syncwarp();
         }
       }
-      load_ids(x);
-      return x;
-    };
-    uint2 qraw[HN];
-    auto load_query = [&](int s) {
-      const T* q = static_cast<const T*>(P.q) +
-                   (static_cast<size_t>(s) * P.num_q_heads + h0) * D + 4 * lane;
-#pragma unroll
-      for (int h = 0; h < HN; ++h)
-        qraw[h] = h < hc ? __ldg(reinterpret_cast<const uint2*>(q + h * D)) : make_uint2(0, 0);
-    };
-    // the 16 lanes of K and of V take the scales of 8 tokens each
-    const int chunk_page = 8 * (lane & 15) / BS, chunk_off = 8 * (lane & 15) - chunk_page * BS;
-    const __nv_bfloat16* scale_src =
-        (lane < 16 ? P.k_scales : P.v_scales) + static_cast<size_t>(g) * BS + chunk_off;
-    const uint32_t scale_dst = smem_addr(scales + (lane >> 4) * kTile + 8 * (lane & 15));
-    const size_t scale_block = static_cast<size_t>(P.num_kv_heads) * BS;
-    load_lens(sp.s);
-    Window now{sp.s, len_of(sp.s), sp.tile * pages / 32 * 32, -1};
-    load_ids(now);
-    load_query(now.s);
-    Window next = next_window(now);
-    int tile = sp.tile, first_tile = tile, seg = 0, np_before = 0;
-    bool first = true;
-    const uint32_t step = BS * 128;
-    auto load_v = [&](int j, int np) {  // V(j), np blocks
-      if (elect_one())
-        load_blocks(smem_addr(v_tiles + (j & 1) * kUTileBytes), step, &vmap, bar(kV, j & 1), g * D,
-                    sm.rows[j & 1], np, np * BS * 64);
-      __syncwarp();
-    };
-    int i = 0;
-    for (; i < n; ++i) {
-      const int b = i & 1;
-      const int valid = min(kTile, now.L - tile * kTile);
-      const int at = tile * pages - now.j;   // of the tile's first block in the window
-      const bool block = lane * BS < valid;  // this lane has a block
-      int id = __shfl_sync(0xffffffffu, now.id, (at + lane) & 31);
-      if (block && static_cast<unsigned>(id) >= static_cast<unsigned>(P.num_blocks)) {
-        raise_error(P.err, PKV_DERR_BLOCK_ID);
-        id = -1;
-      }
-      const int np = __popc(__ballot_sync(0xffffffffu, block));
-      // (an id out of range reads zeros, past the cache's end)
-      if (block) reinterpret_cast<int*>(sm.rows[b])[lane] = (id >= 0 ? id : P.num_blocks) * BS;
-      const int cid = __shfl_sync(0xffffffffu, block ? id : -1, chunk_page);
-      __syncwarp();
-      const bool ends = (tile + 1) * kTile >= now.L;  // the sequence ends with this tile
-      const int flags = (first ? kFirst : 0) | (ends || i + 1 == n ? kLast : 0) |
-                        (first_tile == 0 && ends ? kWhole : 0) | (first_tile == 0 ? kSlot1 : 0);
-      const int4 notes = make_int4(flags, now.s, valid, 0);
-      if (i >= 2 && !warp_wait(kS, i - 2)) break;
+      // every product is complete before tensor memory is released
       if (elect_one()) {
-        sm.qslot[b] = (seg & 1) | (first ? 2 : 0);
-        load_blocks(smem_addr(k_tiles + b * kUTileBytes), step, &kmap, bar(kK, b), g * D,
-                    sm.rows[b], np, np * BS * 64);
-        // S(i - 2) is complete, so P(i - 4) had arrived, and with it the softmax warps had read
-        // the slot of scales and notes
-        if (!first) {
-          sm.meta[i & 3] = notes;
-          mbar_arrive(scale_bar(i));
-        }
+        umma_commit(drain_bar);
+        if (!mbar_wait_bounded(drain_bar, 0)) fail();
       }
-      __syncwarp();
-      // scales, by one plain asynchronous copy: TMA takes about as long for 32 bytes as for a
-      // block of codes
-      const uint32_t dst = scale_dst + (i & 3) * (4 * kTile);
-      if (cid >= 0)
-        copy16_async(dst, scale_src + cid * scale_block);
-      else
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-      __syncwarp();
-      copy_async_arrive(scale_bar(i));
-      if (first) {
-        float factor[HN];
-        // the query rows as E4M3 terms.  The buffer's last reader was a product of the sequence
-        // before the last one, no later than S(i - 2).
-        uint8_t* rows = q_rows + (seg & 1) * NC * 128;
+    } else {
+      // ---- scales, notes, queries -----------------------------------------------------------
+      uint2 qraw[HN];
+      auto load_query = [&](int s) {
+        const T* q = static_cast<const T*>(P.q) +
+                     (static_cast<size_t>(s) * P.num_q_heads + h0) * D + 4 * lane;
 #pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          float x[4];
-          const float2 a = Mma<T>::unpack(qraw[h].x), bb = Mma<T>::unpack(qraw[h].y);
-          x[0] = a.x, x[1] = a.y, x[2] = bb.x, x[3] = bb.y;
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-          top = redux_max(top);
-          // |x| 2^(134 - E) < 256 for the exponent field E of the largest; a query that is not
-          // finite becomes NaN, and a scale of zero leaves scores of zero
-          const int E = max(8, static_cast<int>(top >> 23));
-          float up = P.scale_log2 == 0.f ? 0.f : pow2_bits(261 - E);
-          if (E == 255) up = __uint_as_float(0x7fffffffu);
-          factor[h] = P.scale_log2 == 0.f ? 1.f : fabsf(P.scale_log2) * pow2_bits(E - 7);
-          if (factor[h] < FLT_MIN) factor[h] = FLT_MIN;  // masked scores times it stay -inf
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= up;
-#pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]), hi = f32x2_to_e4m3x2(x[2], x[3]);
-            const int row = q * HN + h;
-            *reinterpret_cast<uint32_t*>(rows + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) +
-                                         (lane & 3) * 4) = lo | (hi << 16);
-            const uint32_t w0 = e4m3x2_to_f16x2(lo), w1 = e4m3x2_to_f16x2(hi);
-            const float2 f0 = Mma<__half>::unpack(w0), f1 = Mma<__half>::unpack(w1);
-            x[0] = (x[0] - f0.x) * 16.f;
-            x[1] = (x[1] - f0.y) * 16.f;
-            x[2] = (x[2] - f1.x) * 16.f;
-            x[3] = (x[3] - f1.y) * 16.f;
-          }
-        }
-        fence_proxy_async_smem();
+        for (int h = 0; h < HN; ++h)
+          qraw[h] = h < hc ? __ldg(reinterpret_cast<const uint2*>(q + h * D)) : make_uint2(0, 0);
+      };
+      // the 16 lanes of K and of V take the scales of 8 tokens each
+      const int chunk_page = 8 * (lane & 15) / BS, chunk_off = 8 * (lane & 15) - chunk_page * BS;
+      const __nv_bfloat16* scale_src =
+          (lane < 16 ? P.k_scales : P.v_scales) + static_cast<size_t>(g) * BS + chunk_off;
+      const uint32_t scale_dst = smem_addr(scales + (lane >> 4) * kTile + 8 * (lane & 15));
+      const size_t scale_block = static_cast<size_t>(P.num_kv_heads) * BS;
+      Ids ids;
+      int i = 0, seg = 0, first_tile = sp.tile;
+      if (n > 0) {
+        w.begin(P, sp);
+        load_query(w.s);
+        ids.begin(P, w, pages);
+      }
+      for (; i < n; ++i) {
+        const int valid = min(kTile, w.L - w.tile * kTile);
+        const int id = ids.of(P, w, pages, lane * BS < valid);
+        const int cid = __shfl_sync(0xffffffffu, lane * BS < valid ? id : -1, chunk_page);
+        const int flags = (w.first ? kFirst : 0) | (w.ends() || i + 1 == n ? kLast : 0) |
+                          (first_tile == 0 && w.ends() ? kWhole : 0) |
+                          (first_tile == 0 ? kSlot1 : 0);
+        if (i >= 4 && !warp_wait_bar(scale_free_bar(i), ((i - 4) >> 2) & 1)) break;
+        // (a plain asynchronous copy: TMA takes about as long for 32 bytes as for a block of codes)
+        const uint32_t dst = scale_dst + (i & 3) * (4 * kTile);
+        if (cid >= 0)
+          copy16_async(dst, scale_src + cid * scale_block);
+        else
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
         __syncwarp();
+        copy_async_arrive(scale_bar(i));
+        if (w.first) {
+          // the query rows as E4M3 terms.  The buffer's last reader was a product of the sequence
+          // before the last one, no later than S(i - 2); P(i - 2) follows that.  (P(i - 4) has
+          // arrived: the release of the scales follows it.)
+          if (i >= 2 && !warp_wait(kP, i - 2)) break;
+          uint8_t* rows = q_rows + (seg & 1) * NC * 128;
+#pragma unroll
+          for (int h = 0; h < HN; ++h) {
+            float x[4];
+            const float2 a = Mma<T>::unpack(qraw[h].x), bb = Mma<T>::unpack(qraw[h].y);
+            x[0] = a.x, x[1] = a.y, x[2] = bb.x, x[3] = bb.y;
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+            top = redux_max(top);
+            // |x| 2^(134 - E) < 256 for the exponent field E of the largest; a query that is not
+            // finite becomes NaN, and a scale of zero leaves scores of zero
+            const int E = max(8, static_cast<int>(top >> 23));
+            float up = P.scale_log2 == 0.f ? 0.f : pow2_bits(261 - E);
+            if (E == 255) up = __uint_as_float(0x7fffffffu);
+            float factor = P.scale_log2 == 0.f ? 1.f : fabsf(P.scale_log2) * pow2_bits(E - 7);
+            if (factor < FLT_MIN) factor = FLT_MIN;  // masked scores times it stay -inf
+            if (lane == 0) sm.f[i & 3][h] = factor;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] *= up;
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+              const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]), hi = f32x2_to_e4m3x2(x[2], x[3]);
+              const int row = q * HN + h;
+              *reinterpret_cast<uint32_t*>(rows + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) +
+                                           (lane & 3) * 4) = lo | (hi << 16);
+              const uint32_t w0 = e4m3x2_to_f16x2(lo), w1 = e4m3x2_to_f16x2(hi);
+              const float2 f0 = Mma<__half>::unpack(w0), f1 = Mma<__half>::unpack(w1);
+              x[0] = (x[0] - f0.x) * 16.f;
+              x[1] = (x[1] - f0.y) * 16.f;
+              x[2] = (x[2] - f1.x) * 16.f;
+              x[3] = (x[3] - f1.y) * 16.f;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kQ, seg & 1));
+        }
         if (lane == 0) {
-          mbar_arrive(bar(kQ, seg & 1));
-#pragma unroll
-          for (int h = 0; h < HN; ++h) sm.f[i & 3][h] = factor[h];
-          sm.meta[i & 3] = notes;
+          sm.meta[i & 3] = make_int4(flags, w.s, valid, 0);
           mbar_arrive(scale_bar(i));
         }
         __syncwarp();
-      }
-      // the next tile, and what it needs from global memory
-      if (i + 1 < n) {
-        first = ends;
-        tile = ends ? 0 : tile + 1;
-        if (ends || tile * pages >= now.j + 32) {
-          now = next;
-          next = next_window(next);
-        }
-        if (ends) {
-          load_query(now.s);
-          first_tile = 0;
-          ++seg;
-        }
-      }
-      // V(i - 1), behind K(i)
-      if (i >= 1) {
-        if (i >= 3 && !warp_wait(kO, i - 3)) break;
-        load_v(i - 1, np_before);
-      }
-      np_before = np;
-    }
-    const bool last = i == n && (n < 3 || warp_wait(kO, n - 3));
-    if (last) load_v(n - 1, np_before);
-    // after a wait that ran out, no copy may be in flight when the CTA ends
-    if (!last && lane == 0) {
-      for (int j = max(0, i - 4); j <= min(i, n - 1); ++j)
-        mbar_wait_for(scale_bar(j), (j >> 2) & 1, kWaitLimitNs / 8);
-      for (int j = max(0, i - 2); j <= min(i, n - 1); ++j)
-        mbar_wait_for(bar(kK, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
-      for (int j = max(0, i - 3); j < i - 1; ++j)
-        mbar_wait_for(bar(kV, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ---- products ---------------------------------------------------------------------------
-    const uint64_t dk = smem_desc_sw128(smem_addr(k_tiles), 16, 1024);
-    const uint64_t dv = smem_desc_sw128(smem_addr(v_tiles), 1024, 1024);
-    const uint64_t dq = smem_desc_sw128(smem_addr(q_rows), 16, 1024);
-    const uint64_t dp = smem_desc_plain(smem_addr(p_rows), 128, 128);
-    constexpr uint64_t kSlot = kUTileBytes / 16;
-    int seg = -1, j = 0;
-    for (; j <= n; ++j) {
-      const int b = j & 1;
-      if (j < n) {
-        // S(j) overwrites S(j - 2), which was read before P(j - 2) arrived; this warp waited for
-        // that arrival when it issued O(j - 2)
-        if (!warp_wait(kK, j)) break;
-        const int note = sm.qslot[b];
-        if (note & 2) {
-          ++seg;
-          if (!warp_wait(kQ, seg)) break;
-        }
-        if (elect_one()) {
-          tc_fence_after_sync();
-          const uint64_t a = dk + b * kSlot, q = dq + (note & 1) * (NC * 8);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            umma_f8_ss(tm_s + b * NC, a + kk * 2, q + kk * 2, kIdS, kk > 0 ? 1u : 0u);
-          umma_commit(bar(kS, b));
-        }
-        __syncwarp();
-      }
-      if (j > 0) {
-        // O(i) overwrites O(i - 2), which was read before P(i) arrived
-        const int i = j - 1, bi = i & 1;
-        if (!warp_wait(kV, i) || !warp_wait(kP, i)) break;
-        if (elect_one()) {
-          tc_fence_after_sync();
-          const uint64_t a = dv + bi * kSlot;
-#pragma unroll
-          for (int half = 0; half < NC / 16; ++half) {
-#pragma unroll
-            for (int kk = 0; kk < kTile / 32; ++kk)
-              umma_f8_ss(tm_o + bi * NC + half * 16, a + kk * 256, dp + half * kTile + kk * 32,
-                         kIdO, kk > 0 ? 1u : 0u);
+        if (i + 1 < n) {
+          w.advance(P);
+          if (w.first) {
+            load_query(w.s);
+            first_tile = 0;
+            ++seg;
           }
-          umma_commit(bar(kO, bi));
         }
-        __syncwarp();
       }
-    }
-    // every product is complete before tensor memory is released
-    if (elect_one()) {
-      umma_commit(drain_bar);
-      if (!mbar_wait_bounded(drain_bar, 0)) fail();
+      if (i < n && lane == 0)
+        for (int j = max(0, i - 3); j <= i; ++j)
+          mbar_wait_for(scale_bar(j), (j >> 2) & 1, kWaitLimitNs / 8);
+      __syncwarp();
+      // rows of sequences without a context, dealt out over the ranges
+      for (int s0 = r; s0 < P.num_seqs; s0 += 32 * P.ranges) {
+        const long long s = s0 + static_cast<long long>(lane) * P.ranges;
+        uint32_t empty = __ballot_sync(0xffffffffu, s < P.num_seqs && live_len(P, s) == 0);
+        for (; empty != 0; empty &= empty - 1) {
+          const size_t row = s0 + static_cast<size_t>(__ffs(empty) - 1) * P.ranges;
+          T* out = static_cast<T*>(P.out) + (row * P.num_q_heads + h0) * D;
+          for (int e = lane; e < hc * D; e += 32) out[e] = from_f32<T>(0.f);
+        }
+      }
     }
     __syncwarp();
   } else {
     // ---- softmax: token tid of S^T, dimension tid of O^T -----------------------------------
+    more_registers<kManyRegs>();
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
     float f[HN], acc[HN], l[HN], m[HN], beta[HN];
     const float sign = P.scale_log2 < 0.f ? -1.f : 1.f;
@@ -695,7 +763,10 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kP, b));
+      if (lane == 0) {
+        mbar_arrive(bar(kP, b));
+        mbar_arrive(scale_free_bar(i));
+      }
       // the output of the tile before, of the same sequence, while the tensor cores work on
       // this one's; it is read before P(i + 1) arrives, which lets O(i + 1) overwrite it
       if (!(flags & kFirst) && ok) add_output(i - 1);
