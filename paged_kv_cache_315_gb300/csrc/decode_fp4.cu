@@ -64,15 +64,38 @@ __device__ __forceinline__ int live_len(const Fp4Params& P, int s) {
   return L < 0 ? 0 : min(L, cap);
 }
 
-__device__ __forceinline__ long long range_begin(long long total, int ranges, int r) {
-  return total * r / ranges;
+// Quotient of non-negative numbers, mostly small ones (a 64-bit division takes three times as
+// long).
+__device__ __forceinline__ long long divide(long long a, int b) {
+  return (a >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                        : a / b;
 }
+
+// `total` tiles over `ranges` ranges: the first `extra` of them hold base + 1 tiles each, the
+// others base.
+struct Cut {
+  long long base;
+  int extra;
+  __device__ __forceinline__ Cut(long long total, int ranges) {
+    base = ranges > 0 ? divide(total, ranges) : 0;
+    extra = static_cast<int>(total - base * ranges);
+  }
+  __device__ __forceinline__ long long begin(int r) const { return base * r + min(r, extra); }
+  // The range that holds tile x.
+  __device__ __forceinline__ int of(long long x) const {
+    const long long big = (base + 1) * extra;
+    return static_cast<int>(x < big ? x / (base + 1) : extra + (x - big) / base);
+  }
+};
 
 // Finds range r; called by all THREADS threads of the CTA.  `notes` (one CTA of each range):
 // say so where a context length is outside the block table, and leave P.info[r], which the
 // merge grid reads: the sequence that begins in the range and goes on past it, if there is one.
+// `lens` (shared memory, may be null) receives the context lengths of the range's first sequence
+// and of the kLens - 1 behind it.
+constexpr int kLens = 64;
 template <int THREADS>
-__device__ Span find_span(const Fp4Params& P, int r, bool notes) {
+__device__ Span find_span(const Fp4Params& P, int r, bool notes, int* lens) {
   constexpr int W = THREADS / 32;
   __shared__ long long warp_tot[W];
   __shared__ int found_s, found_tile;
@@ -105,9 +128,9 @@ __device__ Span find_span(const Fp4Params& P, int r, bool notes) {
   Span sp;
   sp.total = total;
   sp.ranges = static_cast<int>(min(static_cast<long long>(P.ranges), total));
-  sp.begin = r < sp.ranges ? range_begin(total, sp.ranges, r) : total;
-  sp.tiles =
-      r < sp.ranges ? static_cast<int>(range_begin(total, sp.ranges, r + 1) - sp.begin) : 0;
+  const Cut ranges(total, sp.ranges);
+  sp.begin = r < sp.ranges ? ranges.begin(r) : total;
+  sp.tiles = r < sp.ranges ? static_cast<int>(ranges.begin(r + 1) - sp.begin) : 0;
   const long long at = before + incl - own, end = sp.begin + sp.tiles;
   // the sequence that holds tile `x`, one of this thread's, and the first tile of it
   auto holder = [&](long long x, long long& first, int& tiles) {
@@ -126,15 +149,17 @@ __device__ Span find_span(const Fp4Params& P, int r, bool notes) {
   }
   if (notes && sp.tiles > 0 && at < end && end < at + own) {
     const int s = holder(end, first, tiles);
-    // begins in the range and goes on: its last tile lies in the last range that begins at or
-    // before that tile
-    if (first >= sp.begin && first < end)
-      cut = make_int2(s, static_cast<int>(((first + tiles) * sp.ranges + total - 1) / total) - 1);
+    if (first >= sp.begin && first < end)  // begins in the range and goes on past it
+      cut = make_int2(s, ranges.of(first + tiles - 1));
   }
   __syncthreads();
   if (notes && tid == 0 && P.ranges > 1) P.info[r] = cut;
   sp.s = sp.tiles > 0 ? found_s : 0;
   sp.tile = sp.tiles > 0 ? found_tile : 0;
+  if (lens != nullptr) {
+    for (int s = max(s0, sp.s); s < min(s1, sp.s + kLens); ++s) lens[s - sp.s] = live_len(P, s);
+    __syncthreads();
+  }
   return sp;
 }
 
@@ -218,7 +243,8 @@ __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4
   const int g = u / P.num_chunks, c = u - g * P.num_chunks;
   const int h0 = g * P.group + c * P.chunk, hc = min(P.chunk, P.group - c * P.chunk);
   const int BS = P.block_size;
-  const Span sp = find_span<kSimtThreads>(P, r, u == 0);
+  griddep_wait();
+  const Span sp = find_span<kSimtThreads>(P, r, u == 0, nullptr);
   zero_empty_rows<T>(P, D, r, h0, hc, tid, kSimtThreads);
 
   int s = sp.s, tile = sp.tile, left = sp.tiles;
@@ -326,6 +352,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const Fp4Pa
   __shared__ float o_s[kMergeWarps][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = blockIdx.x, head = blockIdx.y;
+  // No early launch of the grid behind this one: a decode CTA placed between merge CTAs leaves
+  // their registers as gaps too small for a third decode CTA on the SM, and the CTAs left over run
+  // after all others (32 contexts of 32k tokens: 277 us a call for 173).
   griddep_wait();
   const int2 info = __ldcg(&P.info[r]);
   if (info.x < 0) return;
@@ -535,6 +564,16 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
                       : a.dtype == PKV_BF16 ? merge_for<__nv_bfloat16>(a.head_dim)
                                             : merge_for<__half>(a.head_dim);
   if (!fn || !merge) return PKV_EUNSUPPORTED;
+  // Both grids may be launched while the grid ahead of them drains, and wait for its end on the
+  // device before they touch memory: that hides the launches and the first grid's set-up.
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
   if (uses_umma(a)) {
     CUtensorMap kmap, vmap;
     const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
@@ -547,22 +586,17 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(ufn),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return PKV_ECUDA;
-    ufn<<<static_cast<unsigned>(grid), kUThreads, smem, stream>>>(kmap, vmap, P);
+    cfg.blockDim = dim3(kUThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    if (cudaLaunchKernelEx(&cfg, ufn, kmap, vmap, P) != cudaSuccess) return PKV_ECUDA;
   } else {
-    fn<<<static_cast<unsigned>(grid), kSimtThreads, 0, stream>>>(P);
+    cfg.blockDim = dim3(kSimtThreads);
+    if (cudaLaunchKernelEx(&cfg, fn, P) != cudaSuccess) return PKV_ECUDA;
   }
-  if (cudaGetLastError() != cudaSuccess) return PKV_ECUDA;
   if (w.ranges > 1) {
-    // launched behind the decode grid while it still runs; its CTAs wait for that grid's end
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(w.ranges - 1), static_cast<unsigned>(a.num_q_heads));
     cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.stream = stream;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, merge, P) != cudaSuccess) return PKV_ECUDA;
   }
   return PKV_OK;

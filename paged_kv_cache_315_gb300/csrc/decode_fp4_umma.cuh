@@ -38,8 +38,7 @@
 //   - the K slot of tile i by S(i), the V slot and the P buffer by O(i);
 //   - the S buffer by P(i), which follows its reading; S(i + 2) waits for it;
 //   - the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives;
-//   - scales and notes by a barrier of their own, a query buffer by the P of the last tile that
-//     used it.
+//   - scales and notes by a barrier of their own, a query buffer by the last S that reads it.
 // A wait by parity must not be lapped: a warp may wait for a barrier's use by tile i only while
 // the use by the next tile of that slot cannot complete without the warp itself (K(i + 2) is what
 // S(i + 2) waits for, V(i + 2) what O(i + 2) does, scales(i + 2) what P(i + 2) does).
@@ -47,7 +46,7 @@
 // chains have to stay below that one by one.  With all loads in one warp that warp was the bound
 // (16 TMA copies of a 16-token block each, at 45-60 clocks from an elected thread in straight-line
 // code, 80 from eight lanes side by side).  The registers follow the roles: 80 a thread at launch,
-// then 96 for softmax warps and 64 for the others.
+// then 88 for softmax warps and 72 for the others.
 
 constexpr int kUTileBytes = kTile * 128;  // a K or V tile in shared memory (64 of 128 bytes data)
 constexpr int kUThreads = 256;
@@ -59,24 +58,24 @@ template <typename T>
 constexpr int u_terms() { return std::is_same<T, __half>::value ? 3 : 2; }
 __host__ __device__ constexpr int u_cols(int terms, int HN) { return terms * HN <= 16 ? 16 : 32; }
 __host__ __device__ constexpr int u_smem(int NC) {
-  return 1024 + 4 * kUTileBytes + 2 * NC * 128 + NC * kTile + kUScaleBytes + 1088;
+  return 1024 + 4 * kUTileBytes + 2 * NC * 128 + NC * kTile + kUScaleBytes + 1600;
 }
 
 // What the warps tell each other, behind the tiles.
 struct USmem {
   int4 meta[4];          // per tile: flags, sequence, live tokens
-  float f[4][kHeads];    // per tile, first of a sequence: score factor of each head
+  float f[4][2][kHeads]; // per sequence: score factor of each head, and its negative
   float top[2][4][kHeads];
   uint32_t vtop[2][4];
-  float lsum[4][kHeads];
-  uint64_t bars[21];
+  float lsum[2][4][kHeads];  // per sequence: the warps' sums of weights
+  uint64_t bars[23];
+  int lens[kLens];       // of the range's first sequence and those behind it
   int4 rows[2][4];       // of K, of V: the cache row of each block of a tile
   uint32_t tmem;
-  volatile int abort;
 };
-static_assert(sizeof(USmem) <= 1088, "bookkeeping area");
+static_assert(sizeof(USmem) <= 1600, "bookkeeping area");
 
-enum { kFirst = 1, kLast = 2, kWhole = 4, kSlot1 = 8 };
+enum { kFirst = 1, kLast = 2, kWhole = 4, kSlot1 = 8, kSeqShift = 4 };  // and sequence mod 4
 
 __device__ __forceinline__ float redux_max(float v) {
   float r;
@@ -138,6 +137,29 @@ __device__ __forceinline__ void load_blocks(uint32_t dst, uint32_t step, const C
 
 __device__ __forceinline__ float pow2_bits(int field) {
   return __uint_as_float(static_cast<uint32_t>(field) << 23);
+}
+
+// Combines the lanes' values of each head: every step halves the heads a lane still holds, so H
+// heads take H + 4 - log2(H) exchanges instead of 5 H.  Returns head lane / (32 / H)'s result.
+template <int H, typename Op>
+__device__ __forceinline__ float reduce_heads(const float (&v)[H], Op op) {
+  const int lane = threadIdx.x & 31;
+  float x[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) x[h] = v[h];
+  int o = 16;
+#pragma unroll
+  for (int c = H / 2; c > 0; c >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int h = 0; h < c; ++h) {
+      const float give = up ? x[h] : x[h + c], keep = up ? x[h + c] : x[h];
+      x[h] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
+  return x[0];
 }
 
 // Two fp32 operations in one instruction, on neighbouring heads; H = 1 has no pair.
@@ -238,6 +260,29 @@ __device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], float (
   if constexpr (NT == 3) fma_heads(v, t[2], 0.00390625f, v);
 }
 
+// Waits for the phase of `bar` with the given parity like mbar_wait_bounded, but lets the
+// hardware hold the thread for up to 20 us at a time: eight warps share four issue slots with the
+// softmax, and a spinning warp takes as many of them as a working one.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+  auto attempt = [&]() {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000)
+        : "memory");
+    return done != 0;
+  };
+  if (attempt()) return true;
+  const unsigned long long t0 = global_timer_ns();
+  do {
+    if (attempt()) return true;
+  } while (global_timer_ns() - t0 < kWaitLimitNs);
+  return false;
+}
+
 // Registers of a thread from here on, for the four warps of a warpgroup.
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -248,83 +293,76 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The tiles of a range in order, walked by a whole warp.
+// The context lengths that a range's walks meet, the first kLens of them in shared memory.
+struct Lens {
+  const int* near;
+  int s0;
+  __device__ __forceinline__ int of(const Fp4Params& P, int s) const {
+    return s - s0 < kLens ? near[s - s0] : live_len(P, s);
+  }
+};
+
+// The tiles of a range in order.
 struct Walk {
   int s, L, tile;  // the tile's sequence, its context length, the tile within it
   bool first;      // the sequence's first tile in this range
-  int lens_at, lens;
 
-  __device__ __forceinline__ int len_of(const Fp4Params& P, int x) {
-    const int lane = threadIdx.x & 31;
-    if (x >= lens_at + 32) {  // 32 lengths at a time, one per lane
-      lens_at = x;
-      lens = x + lane < P.num_seqs ? live_len(P, x + lane) : 0;
-    }
-    return __shfl_sync(0xffffffffu, lens, x - lens_at);
-  }
-  __device__ __forceinline__ void begin(const Fp4Params& P, const Span& sp) {
-    lens_at = sp.s - 32;
-    s = sp.s;
-    L = len_of(P, s);
-    tile = sp.tile;
-    first = true;
+  __device__ __forceinline__ void next_sequence(const Fp4Params& P, const Lens& lens) {
+    do {
+      L = lens.of(P, ++s);
+    } while (L == 0);
+    tile = 0;
   }
   // the sequence ends with this tile
   __device__ __forceinline__ bool ends() const { return (tile + 1) * kTile >= L; }
   // (not called behind the range's last tile: a sequence with tiles follows)
-  __device__ __forceinline__ void advance(const Fp4Params& P) {
+  __device__ __forceinline__ void advance(const Fp4Params& P, const Lens& lens) {
     first = ends();
-    if (first) {
-      do {
-        L = len_of(P, ++s);
-      } while (L == 0);
-      tile = 0;
-    } else {
+    if (first)
+      next_sequence(P, lens);
+    else
       ++tile;
-    }
   }
 };
 
 // The block ids of a range's tiles.  They come 32 at a time, one per lane, and one window ahead:
 // under load a row of the block table takes longer to arrive than a tile takes.
 struct Ids {
-  int s, j, id;     // the lane's id is that of logical block j + lane of sequence s
-  int ns, nj, nid;  // the window behind it
-  Walk ahead;       // at the sequence of the window behind
+  int s, j, id;         // the lane's id is that of logical block j + lane of sequence s
+  int ns, nj, nid, nL;  // the window behind it, and its sequence's length
 
   __device__ __forceinline__ int load(const Fp4Params& P, int seq, int L, int j0) const {
     const int x = j0 + static_cast<int>(threadIdx.x & 31);
-    return seq < P.num_seqs && static_cast<long long>(x) * P.block_size < L
+    return static_cast<long long>(x) * P.block_size < L
                ? __ldg(&P.block_tables[static_cast<size_t>(seq) * P.max_blocks_per_seq + x])
                : -1;
   }
-  __device__ __forceinline__ void load_next(const Fp4Params& P) {
-    ns = ahead.s;
+  __device__ __forceinline__ void load_next(const Fp4Params& P, const Lens& lens) {
     nj = j + 32;
-    if (static_cast<long long>(nj) * P.block_size >= ahead.L) {
-      nj = 0;
-      ahead.L = 0;
-      while (++ahead.s < P.num_seqs && (ahead.L = ahead.len_of(P, ahead.s)) == 0) {
+    if (static_cast<long long>(nj) * P.block_size >= nL) {
+      nj = nL = 0;
+      while (++ns < P.num_seqs && (nL = lens.of(P, ns)) == 0) {
       }
-      ns = ahead.s;
     }
-    nid = load(P, ns, ahead.L, nj);
+    nid = load(P, ns, nL, nj);
   }
-  __device__ __forceinline__ void begin(const Fp4Params& P, const Walk& w, int pages) {
-    ahead = w;
-    s = w.s;
+  __device__ __forceinline__ void begin(const Fp4Params& P, const Lens& lens, const Walk& w,
+                                        int pages) {
+    s = ns = w.s;
+    nL = w.L;
     j = w.tile * pages / 32 * 32;
     id = load(P, s, w.L, j);
-    load_next(P);
+    load_next(P, lens);
   }
   // This lane's block of the walk's tile, `block` saying whether it has one: its id, or -1 (and
   // an error) where that is out of range.
-  __device__ __forceinline__ int of(const Fp4Params& P, const Walk& w, int pages, bool block) {
+  __device__ __forceinline__ int of(const Fp4Params& P, const Lens& lens, const Walk& w, int pages,
+                                    bool block) {
     if (w.s != s || w.tile * pages >= j + 32) {
       s = ns;
       j = nj;
       id = nid;
-      load_next(P);
+      load_next(P, lens);
     }
     int x = __shfl_sync(0xffffffffu, id, (w.tile * pages - j + (threadIdx.x & 31)) & 31);
     if (block && static_cast<unsigned>(x) >= static_cast<unsigned>(P.num_blocks)) {
@@ -347,7 +385,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   constexpr uint32_t kIdO = umma_idesc_e2m1_e4m3(D, 16, true, true);
   constexpr uint32_t kTmemCols = NC == 16 ? 64 : 128;
   // 4 (kManyRegs + kFewRegs) registers of 4 warps are what 8 warps have at launch: 80 or 128 each
-  constexpr int kManyRegs = NC == 16 ? 96 : 168, kFewRegs = NC == 16 ? 64 : 88;
+  constexpr int kManyRegs = NC == 16 ? 88 : 168, kFewRegs = NC == 16 ? 72 : 88;
   extern __shared__ uint8_t smem_raw[];
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -369,13 +407,13 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   auto bar = [&](int kind, int slot) { return smem_addr(&sm.bars[2 * kind + slot]); };
   auto scale_bar = [&](int i) { return smem_addr(&sm.bars[12 + (i & 3)]); };
   auto scale_free_bar = [&](int i) { return smem_addr(&sm.bars[16 + (i & 3)]); };
-  const uint32_t drain_bar = smem_addr(&sm.bars[20]);
+  auto query_free_bar = [&](int seg) { return smem_addr(&sm.bars[20 + (seg & 1)]); };
+  const uint32_t drain_bar = smem_addr(&sm.bars[22]);
 
   if (tid == 0) {
-    for (int k = 0; k < 21; ++k)  // scales: an arrival of each lane, and one for the notes
+    for (int k = 0; k < 23; ++k)  // scales: an arrival of each lane, and one for the notes
       mbar_init(smem_addr(&sm.bars[k]),
                 k / 2 == kP || (k >= 16 && k < 20) ? 4 : k >= 12 && k < 16 ? 33 : 1);
-    sm.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
@@ -389,24 +427,21 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     tmem_relinquish();
   }
   tc_fence_before_sync();
+  griddep_wait();  // nothing above depends on what the grid ahead writes
   // (synchronises all threads; u == 0 also leaves the merge's notes)
-  const Span sp = find_span<kUThreads>(P, r, u == 0);
+  const Span sp = find_span<kUThreads>(P, r, u == 0, sm.lens);
   tc_fence_after_sync();
   const int n = sp.tiles;
   const uint32_t tm_s = sm.tmem, tm_o = tm_s + 2 * NC;
 
-  auto fail = [&]() {
-    raise_error(P.err, PKV_DERR_TIMEOUT);
-    sm.abort = 1;
-  };
-  // A whole warp's wait for tile i's use of a two-slot barrier; false after an abort.  Mostly
-  // the phase is complete already.
+  // A wait ran out (the call's output is void): the warp ends its role, and the others' waits for
+  // it run out in turn.
+  auto fail = [&]() { raise_error(P.err, PKV_DERR_TIMEOUT); };
+  // A whole warp's wait for tile i's use of a two-slot barrier; false when it ran out.
   auto warp_wait_bar = [&](uint32_t at, uint32_t parity) -> bool {
-    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(at, parity));
+    const bool ok = __all_sync(0xffffffffu, wait_phase(at, parity));
     if (!ok && lane == 0) fail();
-    __syncwarp();
-    return !__any_sync(0xffffffffu, sm.abort != 0);
+    return ok;
   };
   auto warp_wait = [&](int kind, int i) {
     return warp_wait_bar(bar(kind, i & 1), (i >> 1) & 1);
@@ -415,7 +450,8 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   if (warp >= 4) {
     fewer_registers<kFewRegs>();
     const int pages = kTile / BS;
-    Walk w;
+    const Lens lens{sm.lens, sp.s};
+    Walk w{sp.s, n > 0 ? sm.lens[0] : 0, sp.tile, true};
     if (warp == 4 || warp == 6) {
       // ---- K tiles (warp 4), V tiles (warp 6) ----------------------------------------------
       const bool is_k = warp == 4;
@@ -425,16 +461,13 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       int4* rows = sm.rows[is_k ? 0 : 1];
       Ids ids;
       int i = 0;
-      if (n > 0) {
-        w.begin(P, sp);
-        ids.begin(P, w, pages);
-      }
+      if (n > 0) ids.begin(P, lens, w, pages);
       for (; i < n; ++i) {
         const int b = i & 1;
         const int valid = min(kTile, w.L - w.tile * kTile);
         const bool block = lane * BS < valid;  // this lane has a block
         const int np = (valid + BS - 1) / BS;
-        const int id = ids.of(P, w, pages, block);
+        const int id = ids.of(P, lens, w, pages, block);
         // (an id out of range reads zeros, past the cache's end)
         if (block) reinterpret_cast<int*>(rows)[lane] = (id >= 0 ? id : P.num_blocks) * BS;
         __syncwarp();
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
           load_blocks(tiles + b * kUTileBytes, BS * 128, map, bar(kind, b), g * D, rows, np,
                       np * BS * 64);
         __syncwarp();
-        if (i + 1 < n) w.advance(P);
+        if (i + 1 < n) w.advance(P, lens);
       }
       // after a wait that ran out, no copy may be in flight when the CTA ends
       if (i < n && lane == 0)
@@ -457,7 +490,6 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       const uint64_t dp = smem_desc_plain(smem_addr(p_rows), 128, 128);
       constexpr uint64_t kSlot = kUTileBytes / 16;
       int seg = -1;
-      if (n > 0) w.begin(P, sp);
       for (int j = 0; n > 0 && j <= n; ++j) {
         const int b = j & 1;
         if (j < n) {
@@ -475,9 +507,10 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
             for (int kk = 0; kk < D / 32; ++kk)
               umma_f8_ss(tm_s + b * NC, a + kk * 2, q + kk * 2, kIdS, kk > 0 ? 1u : 0u);
             umma_commit(bar(kS, b));
+            if (w.ends()) umma_commit(query_free_bar(seg));
           }
           __syncwarp();
-          if (j + 1 < n) w.advance(P);
+          if (j + 1 < n) w.advance(P, lens);
         }
         if (j > 0) {
           // O(i) overwrites O(i - 2), which was read before P(i) arrived
@@ -505,13 +538,72 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       }
     } else {
       // ---- scales, notes, queries -----------------------------------------------------------
+      // Queries are prepared one sequence ahead: `query` walks the sequences, whose first tile is
+      // the range's tile `query_at`.
+      Walk query = w;
+      int query_at = 0, query_seg = 0;
       uint2 qraw[HN];
-      auto load_query = [&](int s) {
+      auto load_query = [&]() {
         const T* q = static_cast<const T*>(P.q) +
-                     (static_cast<size_t>(s) * P.num_q_heads + h0) * D + 4 * lane;
+                     (static_cast<size_t>(query.s) * P.num_q_heads + h0) * D + 4 * lane;
 #pragma unroll
         for (int h = 0; h < HN; ++h)
           qraw[h] = h < hc ? __ldg(reinterpret_cast<const uint2*>(q + h * D)) : make_uint2(0, 0);
+      };
+      // The query rows as E4M3 terms; false when a wait ran out.
+      auto put_query = [&]() -> bool {
+        const int buf = query_seg & 1;
+        if (query_seg >= 2 && !warp_wait_bar(query_free_bar(buf), ((query_seg - 2) >> 1) & 1))
+          return false;
+        uint8_t* rows = q_rows + buf * NC * 128;
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          float x[4];
+          const float2 a = Mma<T>::unpack(qraw[h].x), bb = Mma<T>::unpack(qraw[h].y);
+          x[0] = a.x, x[1] = a.y, x[2] = bb.x, x[3] = bb.y;
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+          top = redux_max(top);
+          // |x| 2^(134 - E) < 256 for the exponent field E of the largest; a query that is not
+          // finite becomes NaN, and a scale of zero leaves scores of zero
+          const int E = max(8, static_cast<int>(top >> 23));
+          float up = P.scale_log2 == 0.f ? 0.f : pow2_bits(261 - E);
+          if (E == 255) up = __uint_as_float(0x7fffffffu);
+          float factor = P.scale_log2 == 0.f ? 1.f : fabsf(P.scale_log2) * pow2_bits(E - 7);
+          if (factor < FLT_MIN) factor = FLT_MIN;  // masked scores times it stay -inf
+          // (S of the sequence two before is complete, so the softmax warps are done with the one
+          // four before, whose place this is)
+          if (lane == 0) {
+            sm.f[query_seg & 3][0][h] = factor;
+            sm.f[query_seg & 3][1][h] = -factor;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= up;
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]), hi = f32x2_to_e4m3x2(x[2], x[3]);
+            const int row = q * HN + h;
+            *reinterpret_cast<uint32_t*>(rows + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) +
+                                         (lane & 3) * 4) = lo | (hi << 16);
+            const uint32_t w0 = e4m3x2_to_f16x2(lo), w1 = e4m3x2_to_f16x2(hi);
+            const float2 f0 = Mma<__half>::unpack(w0), f1 = Mma<__half>::unpack(w1);
+            x[0] = (x[0] - f0.x) * 16.f;
+            x[1] = (x[1] - f0.y) * 16.f;
+            x[2] = (x[2] - f1.x) * 16.f;
+            x[3] = (x[3] - f1.y) * 16.f;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQ, buf));
+        query_at += (query.L + kTile - 1) / kTile - query.tile;
+        ++query_seg;
+        if (query_at < n) {
+          query.next_sequence(P, lens);
+          load_query();
+        }
+        return true;
       };
       // the 16 lanes of K and of V take the scales of 8 tokens each
       const int chunk_page = 8 * (lane & 15) / BS, chunk_off = 8 * (lane & 15) - chunk_page * BS;
@@ -522,17 +614,17 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       Ids ids;
       int i = 0, seg = 0, first_tile = sp.tile;
       if (n > 0) {
-        w.begin(P, sp);
-        load_query(w.s);
-        ids.begin(P, w, pages);
+        load_query();
+        ids.begin(P, lens, w, pages);
+        put_query();
       }
       for (; i < n; ++i) {
         const int valid = min(kTile, w.L - w.tile * kTile);
-        const int id = ids.of(P, w, pages, lane * BS < valid);
+        const int id = ids.of(P, lens, w, pages, lane * BS < valid);
         const int cid = __shfl_sync(0xffffffffu, lane * BS < valid ? id : -1, chunk_page);
         const int flags = (w.first ? kFirst : 0) | (w.ends() || i + 1 == n ? kLast : 0) |
                           (first_tile == 0 && w.ends() ? kWhole : 0) |
-                          (first_tile == 0 ? kSlot1 : 0);
+                          (first_tile == 0 ? kSlot1 : 0) | (seg & 3) << kSeqShift;
         if (i >= 4 && !warp_wait_bar(scale_free_bar(i), ((i - 4) >> 2) & 1)) break;
         // (a plain asynchronous copy: TMA takes about as long for 32 bytes as for a block of codes)
         const uint32_t dst = scale_dst + (i & 3) * (4 * kTile);
@@ -542,58 +634,16 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
         __syncwarp();
         copy_async_arrive(scale_bar(i));
-        if (w.first) {
-          // the query rows as E4M3 terms.  The buffer's last reader was a product of the sequence
-          // before the last one, no later than S(i - 2); P(i - 2) follows that.  (P(i - 4) has
-          // arrived: the release of the scales follows it.)
-          if (i >= 2 && !warp_wait(kP, i - 2)) break;
-          uint8_t* rows = q_rows + (seg & 1) * NC * 128;
-#pragma unroll
-          for (int h = 0; h < HN; ++h) {
-            float x[4];
-            const float2 a = Mma<T>::unpack(qraw[h].x), bb = Mma<T>::unpack(qraw[h].y);
-            x[0] = a.x, x[1] = a.y, x[2] = bb.x, x[3] = bb.y;
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-            top = redux_max(top);
-            // |x| 2^(134 - E) < 256 for the exponent field E of the largest; a query that is not
-            // finite becomes NaN, and a scale of zero leaves scores of zero
-            const int E = max(8, static_cast<int>(top >> 23));
-            float up = P.scale_log2 == 0.f ? 0.f : pow2_bits(261 - E);
-            if (E == 255) up = __uint_as_float(0x7fffffffu);
-            float factor = P.scale_log2 == 0.f ? 1.f : fabsf(P.scale_log2) * pow2_bits(E - 7);
-            if (factor < FLT_MIN) factor = FLT_MIN;  // masked scores times it stay -inf
-            if (lane == 0) sm.f[i & 3][h] = factor;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] *= up;
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
-              const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]), hi = f32x2_to_e4m3x2(x[2], x[3]);
-              const int row = q * HN + h;
-              *reinterpret_cast<uint32_t*>(rows + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) +
-                                           (lane & 3) * 4) = lo | (hi << 16);
-              const uint32_t w0 = e4m3x2_to_f16x2(lo), w1 = e4m3x2_to_f16x2(hi);
-              const float2 f0 = Mma<__half>::unpack(w0), f1 = Mma<__half>::unpack(w1);
-              x[0] = (x[0] - f0.x) * 16.f;
-              x[1] = (x[1] - f0.y) * 16.f;
-              x[2] = (x[2] - f1.x) * 16.f;
-              x[3] = (x[3] - f1.y) * 16.f;
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kQ, seg & 1));
-        }
         if (lane == 0) {
           sm.meta[i & 3] = make_int4(flags, w.s, valid, 0);
           mbar_arrive(scale_bar(i));
         }
         __syncwarp();
+        // the query of the next sequence, whose buffer frees with the first product of this one
+        if (w.first && query_at < n && !put_query()) break;
         if (i + 1 < n) {
-          w.advance(P);
+          w.advance(P, lens);
           if (w.first) {
-            load_query(w.s);
             first_tile = 0;
             ++seg;
           }
@@ -619,18 +669,25 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     // ---- softmax: token tid of S^T, dimension tid of O^T -----------------------------------
     more_registers<kManyRegs>();
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
-    float f[HN], acc[HN], l[HN], m[HN], beta[HN];
+    // Sums of weights l and outputs acc are relative to a running reference, held as its negative
+    // nm.  A tile's product joins acc one iteration later, when P of the next tile is on its way,
+    // and a sequence's rows are written then too: nothing waits for a product just issued.
+    float acc[HN], l[HN], nm[HN], beta[HN];
     const float sign = P.scale_log2 < 0.f ? -1.f : 1.f;
+    int before = 0, before_s = 0;  // flags and sequence of the tile before
     bool ok = true;
+#pragma unroll
+    for (int h = 0; h < HN; ++h) acc[h] = 0.f;
     // every lane waits; whether all four warps go on is decided at the barriers below
     auto wait_bar = [&](uint32_t at, int parity) -> bool {
-      const bool got = mbar_wait_bounded(at, parity);
+      const bool got = wait_phase(at, parity);
       const bool all = __all_sync(0xffffffffu, got);
       if (!all && lane == 0) fail();
       return all;
     };
     auto wait = [&](int kind, int i) { return wait_bar(bar(kind, i & 1), (i >> 1) & 1); };
-    auto add_output = [&](int i) {  // acc += O(i) beta
+    // acc += O(i) beta; behind a sequence's last tile its rows are written
+    auto add_output = [&](int i) {
       uint32_t o[COLS];
       float v[HN];
       tc_fence_after_sync();
@@ -638,6 +695,25 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       tc_fence_before_sync();
       join_terms<NT, HN>(o, v);
       fma_heads(acc, v, beta, acc);
+      if (!(before & kLast)) return;
+      const int seq = before >> kSeqShift;
+      const float(*lsum)[kHeads] = sm.lsum[seq & 1];
+      const size_t idx =
+          (static_cast<size_t>(r) * 2 + ((before & kSlot1) ? 1 : 0)) * P.num_q_heads + h0;
+      T* out = static_cast<T*>(P.out) + (static_cast<size_t>(before_s) * P.num_q_heads + h0) * D;
+#pragma unroll
+      for (int h = 0; h < HN; ++h) {
+        if (h < hc) {
+          const float den = (lsum[0][h] + lsum[1][h]) + (lsum[2][h] + lsum[3][h]);  // > 0, or NaN
+          if (before & kWhole) {
+            out[h * D + tid] = from_f32<T>(__fdividef(acc[h], den));
+          } else {
+            P.part_o[(idx + h) * D + tid] = acc[h];
+            if (tid == 0) P.part_ml[idx + h].y = den;
+          }
+        }
+        acc[h] = 0.f;
+      }
     };
     for (int i = 0; i < n; ++i) {
       const int b = i & 1;
@@ -647,12 +723,8 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       const __nv_bfloat16* sc = scales + (i & 3) * 2 * kTile + tid;
       const float ks = __bfloat162float(sc[0]) * sign;
       float vs = __bfloat162float(sc[kTile]);
-      if (flags & kFirst) {
-#pragma unroll
-        for (int h = 0; h < HN; ++h) f[h] = sm.f[i & 3][h];
-      }
       ok = ok && wait(kS, i);
-      // scores but for the head's factor f >= 0, which the exponent below applies
+      // scores but for the head's factor f > 0, which the exponent below applies
       float x[HN];
       if (ok) {
         uint32_t sr[COLS];
@@ -684,43 +756,46 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       }
       ok = softmax_sync_and(ok);
       if (!ok) break;
-      float t[HN], nt[HN], d[HN];
+      // (the query's factors are in place: they were written before the first tile's notes)
+      float f[HN], nt[HN], d[HN];  // nt: the tile's reference in log2 units, negated
 #pragma unroll
-      for (int h = 0; h < HN; ++h)
-        t[h] = fmaxf(max3(sm.top[b][0][h], sm.top[b][1][h], sm.top[b][2][h]), sm.top[b][3][h]);
+      for (int h = 0; h < HN; ++h) {
+        f[h] = sm.f[flags >> kSeqShift][1][h];
+        nt[h] = fmaxf(max3(sm.top[b][0][h], sm.top[b][1][h], sm.top[b][2][h]), sm.top[b][3][h]);
+      }
       const uint32_t tv = max(max(sm.vtop[b][0], sm.vtop[b][1]), max(sm.vtop[b][2], sm.vtop[b][3]));
       // |vs| 2^(134 - E) < 256 for the exponent field E of the largest
       const int E = min(254, max(8, static_cast<int>(tv >> 23)));
       const float cv = tv >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : vs * pow2_bits(261 - E);
       const float back = pow2_bits(E - 7);
-      mul_heads(t, t, f);  // in log2 units
+      mul_heads(nt, nt, f);
       if (flags & kFirst) {
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
-          m[h] = t[h];
-          acc[h] = 0.f;
+          nm[h] = nt[h];
           l[h] = 0.f;
         }
       }
-      fma_heads(d, m, -1.f, t);
+      fma_heads(d, nt, -1.f, nm);  // how far the tile's reference exceeds the running one
       float most = d[0];
 #pragma unroll
       for (int h = 1; h < HN; ++h) most = fmaxf(most, d[h]);
       if (most > 64.f) {  // the running reference moves
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
-          const float mn = fmaxf(m[h], t[h]);
-          const float a = fast_exp2(m[h] - mn);
+          const float nn = fminf(nm[h], nt[h]);
+          const float a = fast_exp2(nn - nm[h]);
           acc[h] *= a;
           l[h] *= a;
           beta[h] *= a;
-          m[h] = mn;
-          d[h] = t[h] - mn;
+          nm[h] = nn;
+          d[h] = nn - nt[h];
         }
       }
-      float w[HN];
-      mul_heads(nt, t, -1.f);
+#pragma unroll
+      for (int h = 0; h < HN; ++h) f[h] = sm.f[flags >> kSeqShift][0][h];
       fma_heads(x, x, f, nt);
+      float w[HN];
 #pragma unroll
       for (int h = 0; h < HN; ++h) {
         d[h] = fast_exp2(d[h]);  // from the tile's reference to the running one
@@ -728,9 +803,9 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       }
       fma_heads(l, x, d, l);
       mul_heads(w, x, cv);
-      // the weights' E4M3 terms: byte term * HN + head of the token's row.  O(i - 1) has read
-      // the buffer (at a sequence's first tile it was waited for with the last output).
-      if (!(flags & kFirst)) ok = wait(kO, i - 1);
+      // O(i - 1) has read the buffer of the weights
+      if (i > 0) ok = wait(kO, i - 1);
+      // the weights' E4M3 terms: byte term * HN + head of the token's row
       {
         uint32_t row[NC / 4];
 #pragma unroll
@@ -767,38 +842,30 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         mbar_arrive(bar(kP, b));
         mbar_arrive(scale_free_bar(i));
       }
-      // the output of the tile before, of the same sequence, while the tensor cores work on
-      // this one's; it is read before P(i + 1) arrives, which lets O(i + 1) overwrite it
-      if (!(flags & kFirst) && ok) add_output(i - 1);
+      // the tile before, while the tensor cores work on this one; its O is read before P(i + 1)
+      // arrives, which lets O(i + 1) overwrite it.  (beta is that tile's still.)
+      if (i > 0 && ok) add_output(i - 1);
       mul_heads(beta, d, back);
       if (flags & kLast) {
-        ok = ok && wait(kO, i);
-        if (ok) add_output(i);
+        const float sum = reduce_heads(l, [](float p, float q) { return p + q; });
+        if (lane % (32 / HN) == 0)
+          sm.lsum[(flags >> kSeqShift) & 1][warp][lane / (32 / HN)] = sum;
+        if (!(flags & kWhole) && tid == 0) {
+          const size_t idx =
+              (static_cast<size_t>(r) * 2 + ((flags & kSlot1) ? 1 : 0)) * P.num_q_heads + h0;
 #pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          const float sum = warp_sum(l[h]);
-          if (lane == 0) sm.lsum[warp][h] = sum;
-        }
-        ok = softmax_sync_and(ok);
-        if (!ok) break;
-        const bool whole = flags & kWhole;
-        const size_t idx = (static_cast<size_t>(r) * 2 + ((flags & kSlot1) ? 1 : 0)) *
-                               P.num_q_heads + h0;
-#pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          if (h < hc) {
-            const float den = (sm.lsum[0][h] + sm.lsum[1][h]) + (sm.lsum[2][h] + sm.lsum[3][h]);
-            if (whole) {
-              static_cast<T*>(P.out)[(static_cast<size_t>(meta.y) * P.num_q_heads + h0 + h) * D +
-                                     tid] = from_f32<T>(acc[h] / den);
-            } else {
-              P.part_o[(idx + h) * D + tid] = acc[h];
-              if (tid == 0) P.part_ml[idx + h] = make_float2(m[h], den);
-            }
-          }
+          for (int h = 0; h < HN; ++h)
+            if (h < hc) P.part_ml[idx + h].x = -nm[h];
         }
       }
-      // (a wait that ran out shows at the next of the barriers)
+      before = flags;
+      before_s = meta.y;
+      // (a wait that ran out shows at the next barrier)
+    }
+    if (n > 0) {  // the last tile; every warp comes to this barrier
+      ok = ok && wait(kO, n - 1);
+      ok = softmax_sync_and(ok);
+      if (ok) add_output(n - 1);
     }
     tc_fence_before_sync();
   }
