@@ -499,31 +499,60 @@ def kv_cache_write_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     _check("kv_cache_write_fp8", rc)
 
 
-def _on_current(named) -> None:
-    """The tensors are CUDA tensors, contiguous, of the current device (whose stream the
-    kernels run on)."""
+# The calls below are short enough on the GPU for the time spent here to count, so their checks
+# go over the tensors once and look for names only where one fails.
+
+def _on_current(names: str, tensors) -> int:
+    """The current device's index; raises unless the tensors (named in order by ``names``) are
+    contiguous CUDA tensors of that device, whose stream the kernels run on."""
     here = torch.cuda.current_device()
-    for name, t in named.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    for t in tensors:
+        if not t.is_cuda or t.get_device() != here or not t.is_contiguous():
+            break
+    else:
+        return here
+    for name, t in zip(names.split(), tensors):
+        if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.get_device() != here:
             raise ValueError(f"{name} is on device {t.get_device()}, the current one is {here}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    return here
 
 
-def _scratch(device, nbytes: int, workspace, stream) -> torch.Tensor | None:
-    """The caller's workspace, or one of the binding's.
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
-    While a graph is being captured the binding's is a new one, from the graph's own memory
-    pool: the buffer kept for a stream may be replaced by a larger one later, which a
-    replayed graph would not notice, and two graphs must not share one.
+
+def _scratch(device: int, nbytes: int, workspace, raw: int, stream):
+    """(pointer, bytes) of the caller's workspace or, without one, of the binding's.
+
+    The binding keeps one buffer per (device, stream), like ``workspace_for``, taken from the
+    memory of that stream, so that one replaced by a larger one is not handed out while the
+    stream still uses it.  While a graph is being captured it takes a new one, from the graph's
+    own memory pool: a replayed graph would not notice that its buffer was replaced, and two
+    graphs must not share one.
     """
-    if workspace is not None or nbytes == 0:
-        return workspace
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace_for(device, nbytes, stream)
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        if stream is not None:
+            with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+                return _scratch(device, nbytes, None, raw, None)
+        if torch.cuda.is_current_stream_capturing():
+            # (freed into the graph's pool, where only later work of the same graph can get it)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            workspace = _workspaces.get((device, raw))
+            if workspace is None or workspace.numel() < nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                _workspaces[(device, raw)] = workspace
+        return workspace.data_ptr(), workspace.numel()
+    _on_current("workspace", (workspace,))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _fp4_shapes(k_cache, v_cache, k_scales, v_scales):
@@ -532,32 +561,37 @@ def _fp4_shapes(k_cache, v_cache, k_scales, v_scales):
         raise TypeError("k_cache and v_cache must hold E2M1 codes as torch.uint8")
     if k_scales.dtype != torch.bfloat16 or v_scales.dtype != torch.bfloat16:
         raise TypeError("k_scales and v_scales must be torch.bfloat16")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape [NB, bs, Hkv, D / 2]")
-    NB, bs, Hkv, half = k_cache.shape
-    if tuple(k_scales.shape) != (NB, Hkv, bs) or v_scales.shape != k_scales.shape:
+    NB, bs, Hkv, half = shape
+    if k_scales.shape != (NB, Hkv, bs) or v_scales.shape != (NB, Hkv, bs):
         raise ValueError("k_scales and v_scales must be [NB, Hkv, bs]")
     return NB, bs, Hkv, 2 * half
 
 
-def _fp4_rows(fn, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
+def _fp4_rows(name, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
     NB, bs, Hkv, D = _fp4_shapes(k_cache, v_cache, k_scales, v_scales)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, D) or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v.shape != shape:
         raise ValueError("k and v must be [N, Hkv, D] matching the cache")
-    if k.dtype != v.dtype:
+    dtype = k.dtype
+    if v.dtype != dtype:
         raise TypeError("k and v must share one element type")
-    N = k.shape[0]
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (N,):
+    N = shape[0]
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (N,):
         raise TypeError("slot_mapping must be int64 [N]")
     dt = _dtype(k)
     if N == 0:
         return
-    _on_current({"k": k, "v": v, "k_cache": k_cache, "v_cache": v_cache, "k_scales": k_scales,
-                 "v_scales": v_scales, "slot_mapping": slot_mapping})
-    rc = getattr(load(), fn)(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                             k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), N,
-                             Hkv, D, bs, NB, dt, _stream(stream))
-    _check(fn, rc)
+    here = _on_current("k v k_cache v_cache k_scales v_scales slot_mapping",
+                       (k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping))
+    rc = getattr(_lib or load(), name)(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), slot_mapping.data_ptr(), N, Hkv, D, bs, NB, dt,
+        _raw_stream(stream, here))
+    if rc:
+        raise PagedKVError(name, rc)
 
 
 def kv_cache_write_fp4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -598,35 +632,34 @@ def paged_attn_decode_fp4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
     ``context_lens`` int32 [B].
     """
     NB, bs, Hkv, D = _fp4_shapes(k_cache, v_cache, k_scales, v_scales)
-    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or out.shape != shape:
         raise ValueError("shape mismatch between q, out and the caches")
     if q.dtype != out.dtype:
         raise TypeError("q and out must share one element type")
-    B, Hq, _ = q.shape
+    B, Hq, _ = shape
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    table = block_tables.shape
+    if len(table) != 2 or table[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     dt = _dtype(q)
-    lib = load()
     if B == 0:
         return out
-    tensors = {"out": out, "q": q, "k_cache": k_cache, "v_cache": v_cache, "k_scales": k_scales,
-               "v_scales": v_scales, "block_tables": block_tables, "context_lens": context_lens}
-    if workspace is not None:
-        tensors["workspace"] = workspace
-    _on_current(tensors)
-    MB = block_tables.shape[1]
-    need = lib.paged_attn_decode_fp4_workspace_size(B, Hq, Hkv, D, bs, MB)
-    workspace = _scratch(q.device, need, workspace, stream)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    here = _on_current("out q k_cache v_cache k_scales v_scales block_tables context_lens",
+                       (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens))
+    lib = _lib or load()
+    MB = table[1]
+    raw = _raw_stream(stream, here)
+    ws, ws_bytes = _scratch(
+        here, lib.paged_attn_decode_fp4_workspace_size(B, Hq, Hkv, D, bs, MB), workspace, raw, stream)
     rc = lib.paged_attn_decode_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-        context_lens.data_ptr(), B, Hq, Hkv, D, bs, MB, NB, float(scale), dt, ws_ptr, ws_bytes,
-        _stream(stream))
-    _check("paged_attn_decode_fp4", rc)
+        context_lens.data_ptr(), B, Hq, Hkv, D, bs, MB, NB, float(scale), dt, ws, ws_bytes,
+        raw)
+    if rc:
+        raise PagedKVError("paged_attn_decode_fp4", rc)
     return out
 
 
@@ -646,34 +679,39 @@ def kv_resize_requests(block_tables: torch.Tensor, context_lens: torch.Tensor,
     writes ``slot_mapping`` int64 [rows] (-1 behind the last token) and ``query_start`` int32
     [B + 1].  ``num_blocks`` is the number of blocks of the caches.
     """
-    ints = {"block_tables": block_tables, "context_lens": context_lens,
-            "target_lens": target_lens, "free_ring": free_ring, "pool_state": pool_state}
-    if query_start is not None:
-        ints["query_start"] = query_start
-    for name, t in ints.items():
+    tensors = (block_tables, context_lens, target_lens, free_ring, pool_state)
+    for t in tensors:
         if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
+            raise TypeError("block_tables, context_lens, target_lens, free_ring and pool_state "
+                            "must be int32")
     if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
         raise TypeError("slot_mapping must be int64 [rows]")
-    if block_tables.dim() != 2 or free_ring.dim() != 1 or tuple(pool_state.shape) != (4,):
+    table = block_tables.shape
+    if len(table) != 2 or free_ring.dim() != 1 or pool_state.shape != (4,):
         raise ValueError("block_tables must be [B, MB], free_ring [R] and pool_state [4]")
-    B, MB = block_tables.shape
-    if tuple(context_lens.shape) != (B,) or tuple(target_lens.shape) != (B,):
+    B, MB = table
+    if context_lens.shape != (B,) or target_lens.shape != (B,):
         raise ValueError("context_lens and target_lens must be [B]")
-    if query_start is not None and tuple(query_start.shape) != (B + 1,):
-        raise ValueError("query_start must be [B + 1]")
-    lib = load()
-    tensors = dict(ints, slot_mapping=slot_mapping)
-    if workspace is not None:
-        tensors["workspace"] = workspace
-    _on_current(tensors)
-    workspace = _scratch(block_tables.device, lib.kv_resize_requests_workspace_size(B), workspace,
-                         stream)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    start = None
+    if query_start is not None:
+        if query_start.dtype != torch.int32:
+            raise TypeError("query_start must be int32")
+        if query_start.shape != (B + 1,):
+            raise ValueError("query_start must be [B + 1]")
+        tensors += (slot_mapping, query_start)
+        start = query_start.data_ptr()
+    else:
+        tensors += (slot_mapping,)
+    here = _on_current("block_tables context_lens target_lens free_ring pool_state slot_mapping "
+                       "query_start", tensors)
+    lib = _lib or load()
+    raw = _raw_stream(stream, here)
+    ws, ws_bytes = _scratch(here, lib.kv_resize_requests_workspace_size(B), workspace, raw,
+                            stream)
     rc = lib.kv_resize_requests(
         block_tables.data_ptr(), context_lens.data_ptr(), target_lens.data_ptr(),
-        free_ring.data_ptr(), pool_state.data_ptr(), slot_mapping.data_ptr(),
-        query_start.data_ptr() if query_start is not None else None, B, slot_mapping.shape[0],
-        free_ring.shape[0], int(block_size), MB, int(num_blocks),
-        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream))
-    _check("kv_resize_requests", rc)
+        free_ring.data_ptr(), pool_state.data_ptr(), slot_mapping.data_ptr(), start, B,
+        slot_mapping.shape[0], free_ring.shape[0], int(block_size), MB, int(num_blocks), ws,
+        ws_bytes, raw)
+    if rc:
+        raise PagedKVError("kv_resize_requests", rc)

@@ -359,6 +359,7 @@ int cache_fp4(CacheFp4Args& a, bool write, pkv_stream_t stream) {
   if (a.num_tokens < 0 || a.num_kv_heads <= 0 || a.head_dim <= 0 || a.block_size <= 0 ||
       a.num_blocks <= 0 || !valid_dtype(a.dtype))
     return PKV_EINVAL;
+  if (static_cast<long long>(a.num_blocks) * a.block_size >= INT_MAX) return PKV_EINVAL;
   if (!decode_fp4_supported(a.head_dim, a.block_size)) return PKV_EUNSUPPORTED;
   if (a.num_tokens == 0) return PKV_OK;
   if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.k_scales || !a.v_scales || !a.slot_mapping)

@@ -52,12 +52,30 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[kElems]) {
   }
 }
 
-// The 8 codes (element 0 in the lowest four bits) of x / scale, the IEEE quotient.
+// The 8 codes (element 0 in the lowest four bits) of x / scale, the IEEE quotient.  With r the
+// correctly rounded reciprocal of the scale, y = x r and e = x - y scale (exact in one FMA), y + e r
+// is the correctly rounded quotient (Markstein, 1990): three operations an element where the
+// division takes some ten (and one for the sign, which a negative zero loses).  Scales near the ends of fp32's range, where e or r could leave it, take
+// the division.
 __device__ __forceinline__ uint32_t encode8(const float (&x)[kElems], float scale) {
   uint32_t word = 0;
+  const bool plain = scale > 0x1p-100f && scale < 0x1p100f;
+  if (plain) {
+    const float r = __frcp_rn(scale);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    word |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale)) << (8 * i);
+    for (int i = 0; i < 4; ++i) {
+      const float y0 = x[2 * i] * r, y1 = x[2 * i + 1] * r;
+      const float e0 = fmaf(-y0, scale, x[2 * i]), e1 = fmaf(-y1, scale, x[2 * i + 1]);
+      word |= f32x2_to_e2m1x2(copysignf(fmaf(e0, r, y0), x[2 * i]),
+                              copysignf(fmaf(e1, r, y1), x[2 * i + 1]))
+              << (8 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      word |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale))
+              << (8 * i);
+  }
   return word;
 }
 
@@ -80,7 +98,38 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[kElems], __nv_bflo
   return s > 0.f ? encode8(x, s) : 0u;
 }
 
-// One group of D / 8 lanes per (token, head) row, its key and its value row together.
+// The (token, head) rows a group of lanes takes, `stride` rows apart, without a division in the
+// loop.
+struct RowWalk {
+  long long row;
+  int token, head, heads, step_tokens, step_heads;
+  __device__ __forceinline__ RowWalk(long long first, long long stride, int num_heads)
+      : row(first), heads(num_heads) {
+    token = static_cast<int>(first / heads);
+    head = static_cast<int>(first - static_cast<long long>(token) * heads);
+    step_tokens = static_cast<int>(stride / heads);
+    step_heads = static_cast<int>(stride - static_cast<long long>(step_tokens) * heads);
+  }
+  __device__ __forceinline__ void next(long long stride) {
+    row += stride;
+    token += step_tokens;
+    head += step_heads;
+    if (head >= heads) {
+      head -= heads;
+      ++token;
+    }
+  }
+};
+
+// Place of a row's scale.
+__device__ __forceinline__ size_t scale_at(uint32_t slot, int head, int num_heads, int block_size) {
+  const uint32_t block = slot / static_cast<uint32_t>(block_size);
+  return (static_cast<size_t>(block) * num_heads + head) * block_size +
+         (slot - block * static_cast<uint32_t>(block_size));
+}
+
+// One group of D / 8 lanes per (token, head) row, its key and its value row together; kRows rows
+// are loaded before the first of them is worked on.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     write_fp4_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ kc,
@@ -89,39 +138,49 @@ __global__ void __launch_bounds__(kThreads)
                      long long num_rows, int num_heads, int block_size, long long num_slots,
                      unsigned* err) {
   constexpr int LPR = D / kElems;
+  constexpr int kRows = sizeof(T) == 4 ? 1 : 2;
   const int sub = threadIdx.x % LPR;
   const long long stride = static_cast<long long>(gridDim.x) * (kThreads / LPR);
+  RowWalk w(static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR, stride,
+            num_heads);
   // every lane of a warp runs the same number of iterations: the shuffles are warp-wide
-  const long long first = static_cast<long long>(blockIdx.x) * (kThreads / LPR);
-  for (long long base = first; base < num_rows; base += stride) {
-    const long long row = base + threadIdx.x / LPR;
-    const bool in = row < num_rows;
-    const long long r = in ? row : num_rows - 1;
-    const long long token = r / num_heads;
-    const int head = static_cast<int>(r - token * num_heads);
-    const long long slot = __ldg(&slots[token]);
-    float xk[kElems], xv[kElems];
-    load8(k + r * D + sub * kElems, xk);
-    load8(v + r * D + sub * kElems, xv);
-    __nv_bfloat16 sk, sv;
-    const uint32_t ck = quantise<D>(xk, sk), cv = quantise<D>(xv, sv);
-    if (!in || slot < 0) continue;  // past the last row, or padding
-    if (slot >= num_slots) {
-      if (head == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
-      continue;
+  for (long long base = static_cast<long long>(blockIdx.x) * (kThreads / LPR); base < num_rows;
+       base += kRows * stride) {
+    float xk[kRows][kElems], xv[kRows][kElems];
+    long long slot[kRows];
+    int head[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const bool in = w.row < num_rows;
+      const long long r = in ? w.row : num_rows - 1;
+      slot[u] = in ? __ldg(&slots[w.token]) : -1;
+      head[u] = w.head;
+      load8(k + r * D + sub * kElems, xk[u]);
+      load8(v + r * D + sub * kElems, xv[u]);
+      w.next(stride);
     }
-    const long long at = slot * num_heads + head;
-    *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + sub * 4) = ck;
-    *reinterpret_cast<uint32_t*>(vc + at * (D / 2) + sub * 4) = cv;
-    if (sub == 0) {
-      const long long block = slot / block_size;
-      const long long place = (block * num_heads + head) * block_size + (slot - block * block_size);
-      ks[place] = sk;
-      vs[place] = sv;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      __nv_bfloat16 sk, sv;
+      const uint32_t ck = quantise<D>(xk[u], sk), cv = quantise<D>(xv[u], sv);
+      if (slot[u] < 0) continue;  // padding, or past the last row
+      if (slot[u] >= num_slots) {
+        if (head[u] == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
+        continue;
+      }
+      const long long at = slot[u] * num_heads + head[u];
+      *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + sub * 4) = ck;
+      *reinterpret_cast<uint32_t*>(vc + at * (D / 2) + sub * 4) = cv;
+      if (sub == 0) {
+        const size_t place = scale_at(static_cast<uint32_t>(slot[u]), head[u], num_heads, block_size);
+        ks[place] = sk;
+        vs[place] = sv;
+      }
     }
   }
 }
 
+// Four codes' bytes (8 elements) per thread and row; kRows rows of a thread are in flight together.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     read_fp4_kernel(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc,
@@ -130,31 +189,47 @@ __global__ void __launch_bounds__(kThreads)
                     long long num_rows, int num_heads, int block_size, long long num_slots,
                     unsigned* err) {
   constexpr int LPR = D / kElems;
-  const long long total = num_rows * LPR;
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += stride) {
-    const long long r = i / LPR;
-    const int sub = static_cast<int>(i - r * LPR);
-    const long long token = r / num_heads;
-    const int head = static_cast<int>(r - token * num_heads);
-    const long long slot = __ldg(&slots[token]);
-    if (slot < 0) continue;
-    if (slot >= num_slots) {
-      if (head == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
-      continue;
+  constexpr int kRows = 4;
+  const int sub = threadIdx.x % LPR;
+  const long long stride = static_cast<long long>(gridDim.x) * (kThreads / LPR);
+  RowWalk w(static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR, stride,
+            num_heads);
+  while (w.row < num_rows) {
+    long long row[kRows], slot[kRows];
+    int head[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      row[u] = w.row;
+      head[u] = w.head;
+      slot[u] = w.row < num_rows ? __ldg(&slots[w.token]) : -1;
+      w.next(stride);
     }
-    const long long at = slot * num_heads + head;
-    const long long block = slot / block_size;
-    const long long place = (block * num_heads + head) * block_size + (slot - block * block_size);
-    const uint32_t ck = __ldg(reinterpret_cast<const uint32_t*>(kc + at * (D / 2)) + sub);
-    const uint32_t cv = __ldg(reinterpret_cast<const uint32_t*>(vc + at * (D / 2)) + sub);
-    const float sk = __bfloat162float(ks[place]), sv = __bfloat162float(vs[place]);
-    float x[kElems];
-    decode8(ck, sk, x);
-    store8(k + i * kElems, x);
-    decode8(cv, sv, x);
-    store8(v + i * kElems, x);
+    uint32_t ck[kRows], cv[kRows];
+    float sk[kRows], sv[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (slot[u] >= num_slots) {
+        if (head[u] == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
+        slot[u] = -1;
+      }
+      if (slot[u] >= 0) {
+        const long long at = slot[u] * num_heads + head[u];
+        const size_t place = scale_at(static_cast<uint32_t>(slot[u]), head[u], num_heads, block_size);
+        ck[u] = __ldg(reinterpret_cast<const uint32_t*>(kc + at * (D / 2)) + sub);
+        cv[u] = __ldg(reinterpret_cast<const uint32_t*>(vc + at * (D / 2)) + sub);
+        sk[u] = __bfloat162float(ks[place]);
+        sv[u] = __bfloat162float(vs[place]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (slot[u] < 0) continue;
+      float x[kElems];
+      decode8(ck[u], sk[u], x);
+      store8(k + row[u] * D + sub * kElems, x);
+      decode8(cv[u], sv[u], x);
+      store8(v + row[u] * D + sub * kElems, x);
+    }
   }
 }
 
@@ -172,7 +247,7 @@ int run(const CacheFp4Args& a, bool write, cudaStream_t stream) {
   const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
   const long long per_cta = kThreads / (D / kElems);
   const int grid = static_cast<int>(
-      std::max(1LL, std::min((rows + per_cta - 1) / per_cta, 8LL * sm_count())));
+      std::max(1LL, std::min((rows + per_cta - 1) / per_cta, 6LL * sm_count())));
   uint8_t *kc = static_cast<uint8_t*>(a.k_cache), *vc = static_cast<uint8_t*>(a.v_cache);
   __nv_bfloat16 *ks = static_cast<__nv_bfloat16*>(a.k_scales),
                 *vs = static_cast<__nv_bfloat16*>(a.v_scales);

@@ -12,8 +12,10 @@
 //
 // The work is a few bytes per request and token, far below one launch's latency for any
 // decode batch, so what counts is the number of launches and of dependent memory
-// round trips: one CTA computes the sums, and for small batches the same CTA then moves
-// the entries; larger ones launch a grid for that.
+// round trips.  One launch of a cluster of 8 CTAs does it all: every CTA computes the sums for
+// itself in shared memory, moves its share of the entries, and when all CTAs have read the old
+// lengths (the cluster's barrier) the first one writes the new ones and the pool's state.  Many
+// requests or rows take two grids: one CTA for the sums, then as many as the entries want.
 #include <algorithm>
 #include <climits>
 
@@ -26,10 +28,13 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kMaxClusterSeqs = 8192;     // sums of 128 KB of shared memory
+constexpr int kMaxClusterRows = 1 << 17;  // rows that a cluster's 8192 threads still take quickly
 
-// Header of the workspace, in int32 words; then old[n], grow_off[n + 1], need_off[n + 1],
-// give_off[n + 1].
-enum { kWsHead = 0, kWsCount, kWsTaken, kWsGiven, kWsTokens, kWsWords = 8 };
+struct Totals {
+  int head, count, taken, given, tokens;
+};
 
 struct ResizeParams {
   int32_t* block_tables;
@@ -39,9 +44,18 @@ struct ResizeParams {
   int32_t* pool;
   int64_t* slots;
   int32_t* query_start;
-  int32_t *ws, *old_len, *grow_off, *need_off, *give_off;
+  int32_t* ws;  // two-grid form: Totals, then the sums
   int n, num_rows, ring_size, block_size, max_blocks_per_seq, num_blocks;
   unsigned* err;
+};
+
+constexpr int kWsWords = 8;
+
+// The requests' old lengths (-1: refused) and exclusive sums, n + 1 entries each.
+struct Sums {
+  int32_t *old_len, *grow_off, *need_off, *give_off;
+  __host__ __device__ Sums(int32_t* at, int n)
+      : old_len(at), grow_off(at + n + 1), need_off(at + 2 * (n + 1)), give_off(at + 3 * (n + 1)) {}
 };
 
 struct Counts {
@@ -88,24 +102,26 @@ __device__ __forceinline__ int owner(const int32_t* off, int n, int i) {
 }
 
 // Entries i, i + stride, ... of the slot map, the taken blocks and the returned blocks.
-__device__ __forceinline__ void fill(const ResizeParams& P, long long i, long long stride) {
-  const int head = P.ws[kWsHead], count = P.ws[kWsCount];
-  const int taken = P.ws[kWsTaken], given = P.ws[kWsGiven], tokens = P.ws[kWsTokens];
+__device__ __forceinline__ void fill(const ResizeParams& P, const Sums& S, const Totals& tot,
+                                     long long i, long long stride) {
+  const int head = tot.head, count = tot.count;
+  const int taken = tot.taken, given = tot.given, tokens = tot.tokens;
   const int bs = P.block_size;
   const long long end = static_cast<long long>(P.num_rows) + taken + given;
+#pragma unroll 2
   for (; i < end; i += stride) {
     if (i < P.num_rows) {
       const int row = static_cast<int>(i);
       int64_t slot = -1;
       if (row < tokens) {
-        const int s = owner(P.grow_off, P.n, row);
-        const int old_len = P.old_len[s];
+        const int s = owner(S.grow_off, P.n, row);
+        const int old_len = S.old_len[s];
         if (old_len >= 0) {  // admitted
-          const int pos = old_len + row - P.grow_off[s];
+          const int pos = old_len + row - S.grow_off[s];
           const int j = pos / bs, had = (old_len + bs - 1) / bs;
           const int id =
               j < had ? P.block_tables[static_cast<size_t>(s) * P.max_blocks_per_seq + j]
-                      : P.ring[(static_cast<long long>(head) + P.need_off[s] + j - had) %
+                      : P.ring[(static_cast<long long>(head) + S.need_off[s] + j - had) %
                                P.ring_size];
           if (id >= 0 && id < P.num_blocks)
             slot = static_cast<int64_t>(id) * bs + pos % bs;
@@ -116,45 +132,46 @@ __device__ __forceinline__ void fill(const ResizeParams& P, long long i, long lo
       P.slots[row] = slot;
     } else if (i < static_cast<long long>(P.num_rows) + taken) {
       const int a = static_cast<int>(i - P.num_rows);
-      const int s = owner(P.need_off, P.n, a);
-      const int had = (P.old_len[s] + bs - 1) / bs;
-      P.block_tables[static_cast<size_t>(s) * P.max_blocks_per_seq + had + a - P.need_off[s]] =
+      const int s = owner(S.need_off, P.n, a);
+      const int had = (S.old_len[s] + bs - 1) / bs;
+      P.block_tables[static_cast<size_t>(s) * P.max_blocks_per_seq + had + a - S.need_off[s]] =
           P.ring[(static_cast<long long>(head) + a) % P.ring_size];
     } else {
       const int b = static_cast<int>(i - P.num_rows - taken);
-      const int s = owner(P.give_off, P.n, b);
+      const int s = owner(S.give_off, P.n, b);
       // old_len's blocks end at had; the returned ones are the last give_s of them
-      const int had = (P.old_len[s] + bs - 1) / bs;
-      const int give = P.give_off[s + 1] - P.give_off[s];
+      const int had = (S.old_len[s] + bs - 1) / bs;
+      const int give = S.give_off[s + 1] - S.give_off[s];
       if (static_cast<long long>(count) + b < P.ring_size)
         P.ring[(static_cast<long long>(head) + count + b) % P.ring_size] =
             P.block_tables[static_cast<size_t>(s) * P.max_blocks_per_seq + had - give + b -
-                           P.give_off[s]];
+                           S.give_off[s]];
     }
   }
 }
 
-// One CTA: the three prefix sums, which growths are admitted, the new lengths and the
-// pool's state; with FILL the entries too.
-template <bool FILL>
-__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeParams P) {
-  if (!FILL) griddep_launch_dependents();
+// One CTA's threads: the three prefix sums, which growths are admitted, and the totals.  `report`:
+// say what is wrong with lengths, pool or growths.
+__device__ Totals plan(const ResizeParams& P, const Sums& S, bool report) {
   __shared__ long long tot_grow[kPlanWarps];
   __shared__ int tot_need[kPlanWarps], tot_give[kPlanWarps], most_taken;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int head = P.pool[0], count = P.pool[1];
+  // each thread owns a run of `per` requests
+  const int per = (P.n + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = min(P.n, tid * per), s1 = min(P.n, s0 + per);
+  Counts own{0, 0, 0}, c{0, 0, 0};
+  int old_len = 0, new_len = 0;
+  for (int s = s0; s < s1; ++s) {
+    c = counts_of(P, s, old_len, new_len, report);
+    own = own + c;
+  }
   if (head < 0 || head >= P.ring_size || count < 0 || count > P.ring_size) {
-    if (tid == 0) raise_error(P.err, PKV_DERR_POOL);
+    if (report && tid == 0) raise_error(P.err, PKV_DERR_POOL);
     head = 0;
     count = 0;
   }
   if (tid == 0) most_taken = 0;
-  // each thread owns a run of `per` requests
-  const int per = (P.n + kPlanThreads - 1) / kPlanThreads;
-  const int s0 = min(P.n, tid * per), s1 = min(P.n, s0 + per);
-  Counts own{0, 0, 0};
-  int old_len, new_len;
-  for (int s = s0; s < s1; ++s) own = own + counts_of(P, s, old_len, new_len, true);
   Counts incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -183,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeP
   if (warp > 0) at = at + Counts{tot_grow[warp - 1], tot_need[warp - 1], tot_give[warp - 1]};
   int taken = 0;
   for (int s = s0; s < s1; ++s) {
-    const Counts c = counts_of(P, s, old_len, new_len, false);
+    if (per > 1) c = counts_of(P, s, old_len, new_len, false);
     const Counts next = at + c;
     // a growth is admitted while the rows and, if it takes blocks, the free blocks reach:
     // both sums are over every request before it, so no later growth overtakes a refused one
@@ -191,58 +208,78 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeP
                     (next.grow <= P.num_rows && (c.need == 0 || next.need <= count));
     if (ok)
       taken = c.need > 0 ? next.need : taken;
-    else
+    else if (report)
       raise_error(P.err, PKV_DERR_POOL);
-    P.old_len[s] = ok ? old_len : -1;
-    const int row = static_cast<int>(min(at.grow, static_cast<long long>(INT_MAX)));
-    P.grow_off[s] = row;
-    P.need_off[s] = at.need;
-    P.give_off[s] = at.give;
-    if (P.query_start) P.query_start[s] = row;
-    if (ok) P.context_lens[s] = new_len;
+    S.old_len[s] = ok ? old_len : -1;
+    S.grow_off[s] = static_cast<int>(min(at.grow, static_cast<long long>(INT_MAX)));
+    S.need_off[s] = at.need;
+    S.give_off[s] = at.give;
     at = next;
   }
   if (taken > 0) atomicMax(&most_taken, taken);
-  if (tid == kPlanThreads - 1) {
-    const int last = kPlanWarps - 1;
-    const int rows = static_cast<int>(min(tot_grow[last], static_cast<long long>(INT_MAX)));
-    P.grow_off[P.n] = rows;
-    P.need_off[P.n] = tot_need[last];
-    P.give_off[P.n] = tot_give[last];
-    if (P.query_start) P.query_start[P.n] = rows;
-    P.ws[kWsHead] = head;
-    P.ws[kWsCount] = count;
-    P.ws[kWsGiven] = tot_give[last];
-    P.ws[kWsTokens] = min(rows, P.num_rows);
+  const int last = kPlanWarps - 1;
+  const int rows = static_cast<int>(min(tot_grow[last], static_cast<long long>(INT_MAX)));
+  if (tid == 0) {
+    S.grow_off[P.n] = rows;
+    S.need_off[P.n] = tot_need[last];
+    S.give_off[P.n] = tot_give[last];
   }
   __syncthreads();
+  return {head, count, most_taken, tot_give[last], min(rows, P.num_rows)};
+}
+
+// One CTA's threads: the new lengths, the rows' starts and the pool's state.
+__device__ void commit(const ResizeParams& P, const Sums& S, const Totals& tot) {
+  const int tid = threadIdx.x;
+  for (int s = tid; s <= P.n; s += kPlanThreads) {
+    if (P.query_start) P.query_start[s] = S.grow_off[s];
+    if (s < P.n && S.old_len[s] >= 0) {
+      int old_len, new_len;
+      counts_of(P, s, old_len, new_len, false);
+      P.context_lens[s] = new_len;
+    }
+  }
   if (tid == 0) {
-    const int given = tot_give[kPlanWarps - 1];
-    P.ws[kWsTaken] = most_taken;
-    long long left = static_cast<long long>(count) + given;
+    long long left = static_cast<long long>(tot.count) + tot.given;
     if (left > P.ring_size) {  // more blocks come back than the ring has places for
       raise_error(P.err, PKV_DERR_POOL);
       left = P.ring_size;
     }
-    P.pool[0] = static_cast<int>((static_cast<long long>(head) + most_taken) % P.ring_size);
-    P.pool[1] = static_cast<int>(left - most_taken);
+    P.pool[0] = static_cast<int>((static_cast<long long>(tot.head) + tot.taken) % P.ring_size);
+    P.pool[1] = static_cast<int>(left - tot.taken);
   }
-  if (FILL) {
-    __syncthreads();
-    fill(P, tid, kPlanThreads);
-  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) resize_cluster_kernel(const ResizeParams P) {
+  extern __shared__ int32_t sums[];
+  const Sums S(sums, P.n);
+  const bool first = blockIdx.x == 0;
+  const Totals tot = plan(P, S, first);
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  fill(P, S, tot, blockIdx.x * kPlanThreads + threadIdx.x, gridDim.x * kPlanThreads);
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (first) commit(P, S, tot);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeParams P) {
+  griddep_launch_dependents();
+  const Sums S(P.ws + kWsWords, P.n);
+  const Totals tot = plan(P, S, true);
+  if (threadIdx.x == 0) *reinterpret_cast<Totals*>(P.ws) = tot;
+  commit(P, S, tot);
 }
 
 __global__ void __launch_bounds__(kFillThreads) resize_fill_kernel(const ResizeParams P) {
   griddep_wait();
-  fill(P, static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x,
+  fill(P, Sums(P.ws + kWsWords, P.n), *reinterpret_cast<const Totals*>(P.ws),
+       static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x,
        static_cast<long long>(gridDim.x) * kFillThreads);
 }
 
 }  // namespace
 
 size_t resize_workspace_size(int num_seqs) {
-  return (kWsWords + 4ull * num_seqs + 3) * sizeof(int32_t);
+  return (kWsWords + 4ull * (static_cast<size_t>(num_seqs) + 1)) * sizeof(int32_t);
 }
 
 int launch_resize_requests(const ResizeArgs& a, cudaStream_t stream) {
@@ -255,10 +292,6 @@ int launch_resize_requests(const ResizeArgs& a, cudaStream_t stream) {
   P.slots = a.slot_mapping;
   P.query_start = a.query_start;
   P.ws = static_cast<int32_t*>(a.workspace);
-  P.old_len = P.ws + kWsWords;
-  P.grow_off = P.old_len + a.num_seqs;
-  P.need_off = P.grow_off + a.num_seqs + 1;
-  P.give_off = P.need_off + a.num_seqs + 1;
   P.n = a.num_seqs;
   P.num_rows = a.num_rows;
   P.ring_size = a.ring_size;
@@ -266,8 +299,34 @@ int launch_resize_requests(const ResizeArgs& a, cudaStream_t stream) {
   P.max_blocks_per_seq = a.max_blocks_per_seq;
   P.num_blocks = a.num_blocks;
   P.err = a.err;
-  resize_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (a.num_seqs <= kMaxClusterSeqs && a.num_rows <= kMaxClusterRows) {
+    const int smem = static_cast<int>(4 * sizeof(int32_t) * (a.num_seqs + 1));
+    if (smem > 47 * 1024 &&
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(resize_cluster_kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return PKV_ECUDA;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {kCluster, 1, 1};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    return cudaLaunchKernelEx(&cfg, resize_cluster_kernel, P) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  }
+  resize_plan_kernel<<<1, kPlanThreads, 0, stream>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ECUDA;
+  // rows, and the blocks that they may take; blocks that come back share the threads
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const long long entries = static_cast<long long>(a.num_rows) + a.num_rows / a.block_size + 65536;
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      std::min((entries + kFillThreads - 1) / kFillThreads, 8LL * 152)));
+  cfg.blockDim = dim3(kFillThreads);
+  return cudaLaunchKernelEx(&cfg, resize_fill_kernel, P) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 }  // namespace pkv

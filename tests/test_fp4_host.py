@@ -145,7 +145,7 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     t = torch.zeros(2).as_subclass(Elsewhere)
     with pytest.raises(ValueError, match="device 1"):
-        _binding._on_current({"q": t})
+        _binding._on_current("q", (t,))
 
 
 # ---- the plain implementations ----------------------------------------------------------------

@@ -55,7 +55,8 @@ class Pool:
 
 
 @pytest.mark.parametrize("B,MB,bs,seed", [(1, 4, 16, 1), (3, 7, 1, 2), (33, 9, 16, 3),
-                                          (128, 40, 32, 4), (1500, 5, 64, 5), (5000, 3, 16, 6)])
+                                          (128, 40, 32, 4), (1500, 5, 64, 5), (5000, 3, 16, 6),
+                                          (9000, 2, 16, 7)])
 def test_random_steps(pkv, B, MB, bs, seed):
     rng = np.random.default_rng(seed)
     nb = B * MB
