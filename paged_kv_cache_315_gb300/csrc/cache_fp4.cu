@@ -16,6 +16,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;  // resident at 64 registers; the grids hold no more
 constexpr int kElems = 8;  // elements a lane holds of a row: 16 bytes of a 16-bit type
 
 template <typename T>
@@ -131,7 +132,7 @@ __device__ __forceinline__ size_t scale_at(uint32_t slot, int head, int num_head
 // One group of D / 8 lanes per (token, head) row, its key and its value row together; kRows rows
 // are loaded before the first of them is worked on.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     write_fp4_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ kc,
                      uint8_t* __restrict__ vc, __nv_bfloat16* __restrict__ ks,
                      __nv_bfloat16* __restrict__ vs, const int64_t* __restrict__ slots,
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Four codes' bytes (8 elements) per thread and row; kRows rows of a thread are in flight together.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     read_fp4_kernel(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc,
                     const uint8_t* __restrict__ vc, const __nv_bfloat16* __restrict__ ks,
                     const __nv_bfloat16* __restrict__ vs, const int64_t* __restrict__ slots,
@@ -247,7 +248,7 @@ int run(const CacheFp4Args& a, bool write, cudaStream_t stream) {
   const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
   const long long per_cta = kThreads / (D / kElems);
   const int grid = static_cast<int>(
-      std::max(1LL, std::min((rows + per_cta - 1) / per_cta, 6LL * sm_count())));
+      std::max(1LL, std::min((rows + per_cta - 1) / per_cta, static_cast<long long>(kCtasPerSm) * sm_count())));
   uint8_t *kc = static_cast<uint8_t*>(a.k_cache), *vc = static_cast<uint8_t*>(a.v_cache);
   __nv_bfloat16 *ks = static_cast<__nv_bfloat16*>(a.k_scales),
                 *vs = static_cast<__nv_bfloat16*>(a.v_scales);
