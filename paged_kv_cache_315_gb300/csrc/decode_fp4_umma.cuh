@@ -38,10 +38,13 @@
 //   - the K slot of tile i by S(i), the V slot and the P buffer by O(i);
 //   - the S buffer by P(i), which follows its reading; S(i + 2) waits for it;
 //   - the O buffer by P(i + 2): O(i) is read before P(i + 2) arrives;
-//   - scales and notes by a barrier of their own, a query buffer by the last S that reads it.
+//   - the scales and notes of tile i (four slots) by S(i + 2), which waits for P(i), which follows
+//     their reading; a query buffer by the last S that reads it.
+// The barrier of S(i) also counts the arrival of tile i's scales and notes: one wait for the
+// softmax warps instead of two.
 // A wait by parity must not be lapped: a warp may wait for a barrier's use by tile i only while
-// the use by the next tile of that slot cannot complete without the warp itself (K(i + 2) is what
-// S(i + 2) waits for, V(i + 2) what O(i + 2) does, scales(i + 2) what P(i + 2) does).
+// the use by the next tile of that slot cannot complete without the warp itself (K(i + 2) and
+// scales(i + 2) are what S(i + 2)'s barrier waits for, V(i + 2) what O(i + 2)'s does).
 // HBM's copy bandwidth gives each of three CTAs on an SM 2150 clocks for a tile, and the warps'
 // chains have to stay below that one by one.  With all loads in one warp that warp was the bound
 // (16 TMA copies of a 16-token block each, at 45-60 clocks from an elected thread in straight-line
@@ -62,13 +65,13 @@ __host__ __device__ constexpr int u_smem(int NC) {
 }
 
 // What the warps tell each other, behind the tiles.
-struct USmem {
+struct alignas(16) USmem {
   int4 meta[4];          // per tile: flags, sequence, live tokens
   float f[4][2][kHeads]; // per sequence: score factor of each head, and its negative
   float top[2][4][kHeads];
   uint32_t vtop[2][4];
   float lsum[2][4][kHeads];  // per sequence: the warps' sums of weights
-  uint64_t bars[23];
+  uint64_t bars[15];
   int lens[kLens];       // of the range's first sequence and those behind it
   int4 rows[2][4];       // of K, of V: the cache row of each block of a tile
   uint32_t tmem;
@@ -162,51 +165,32 @@ __device__ __forceinline__ float reduce_heads(const float (&v)[H], Op op) {
   return x[0];
 }
 
-// Two fp32 operations in one instruction, on neighbouring heads; H = 1 has no pair.
-template <int H>
-__device__ __forceinline__ void fma_heads(float (&d)[H], const float (&a)[H], const float (&b)[H],
-                                          const float (&c)[H]) {
-  if constexpr (H == 1) {
-    d[0] = fmaf(a[0], b[0], c[0]);
-  } else {
-#pragma unroll
-    for (int h = 0; h < H; h += 2)
-      asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-          "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-          : "=f"(d[h]), "=f"(d[h + 1])
-          : "f"(a[h]), "f"(a[h + 1]), "f"(b[h]), "f"(b[h + 1]), "f"(c[h]), "f"(c[h + 1]));
-  }
-}
+// Two heads' fp32 values in a register pair, for the instructions that work on both.  (One head
+// alone has a pair's other half unused.)
+using Pair = unsigned long long;
 
-template <int H>
-__device__ __forceinline__ void fma_heads(float (&d)[H], const float (&a)[H], float b,
-                                          const float (&c)[H]) {
-  float bb[H];
-#pragma unroll
-  for (int h = 0; h < H; ++h) bb[h] = b;
-  fma_heads(d, a, bb, c);
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-
-template <int H>
-__device__ __forceinline__ void mul_heads(float (&d)[H], const float (&a)[H], const float (&b)[H]) {
-  if constexpr (H == 1) {
-    d[0] = a[0] * b[0];
-  } else {
-#pragma unroll
-    for (int h = 0; h < H; h += 2)
-      asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-          "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-          : "=f"(d[h]), "=f"(d[h + 1])
-          : "f"(a[h]), "f"(a[h + 1]), "f"(b[h]), "f"(b[h + 1]));
-  }
+__device__ __forceinline__ void split(Pair p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
 }
-
-template <int H>
-__device__ __forceinline__ void mul_heads(float (&d)[H], const float (&a)[H], float b) {
-  float bb[H];
-#pragma unroll
-  for (int h = 0; h < H; ++h) bb[h] = b;
-  mul_heads(d, a, bb);
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -250,35 +234,27 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
 
 // The sum of each head's terms.
 template <int NT, int HN>
-__device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], float (&v)[HN]) {
-  float t[NT][HN];
+__device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], Pair (&v)[(HN + 1) / 2]) {
+  auto term = [&](int q, int h) {
+    return pair(__uint_as_float(r[q * HN + h]), h + 1 < HN ? __uint_as_float(r[q * HN + h + 1]) : 0.f);
+  };
 #pragma unroll
-  for (int q = 0; q < NT; ++q)
-#pragma unroll
-    for (int h = 0; h < HN; ++h) t[q][h] = __uint_as_float(r[q * HN + h]);
-  fma_heads(v, t[1], 0.0625f, t[0]);
-  if constexpr (NT == 3) fma_heads(v, t[2], 0.00390625f, v);
+  for (int h = 0; h < HN; h += 2) {
+    v[h / 2] = fma2(term(1, h), pair(0.0625f, 0.0625f), term(0, h));
+    if constexpr (NT == 3) v[h / 2] = fma2(term(2, h), pair(0.00390625f, 0.00390625f), v[h / 2]);
+  }
 }
 
-// Waits for the phase of `bar` with the given parity like mbar_wait_bounded, but lets the
-// hardware hold the thread for up to 20 us at a time: eight warps share four issue slots with the
-// softmax, and a spinning warp takes as many of them as a working one.
+// Waits for the phase of `bar` with the given parity, at most kWaitLimitNs.  The plain try_wait
+// is one instruction in which the hardware holds the thread for a while (given a time to hold it
+// becomes a loop of its own, with sleeps and clock reads).
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-  auto attempt = [&]() {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(20000)
-        : "memory");
-    return done != 0;
-  };
-  if (attempt()) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_timer_ns();
   do {
-    if (attempt()) return true;
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
   } while (global_timer_ns() - t0 < kWaitLimitNs);
   return false;
 }
@@ -401,19 +377,16 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   uint8_t* p_rows = q_rows + 2 * NC * 128;            // [NC / 16][128 tokens][16]
   __nv_bfloat16* scales = reinterpret_cast<__nv_bfloat16*>(p_rows + NC * kTile);
   USmem& sm = *reinterpret_cast<USmem*>(reinterpret_cast<uint8_t*>(scales) + kUScaleBytes);
-  // barriers: K, V loaded, S, O complete, P written, Q written (two slots each), scales (four),
-  // drain
+  // barriers: K, V loaded, S, O complete, P written, Q written, Q read (two slots each), drain
   enum { kK = 0, kV, kS, kP, kO, kQ };
   auto bar = [&](int kind, int slot) { return smem_addr(&sm.bars[2 * kind + slot]); };
-  auto scale_bar = [&](int i) { return smem_addr(&sm.bars[12 + (i & 3)]); };
-  auto scale_free_bar = [&](int i) { return smem_addr(&sm.bars[16 + (i & 3)]); };
-  auto query_free_bar = [&](int seg) { return smem_addr(&sm.bars[20 + (seg & 1)]); };
-  const uint32_t drain_bar = smem_addr(&sm.bars[22]);
+  auto query_free_bar = [&](int seg) { return smem_addr(&sm.bars[12 + (seg & 1)]); };
+  const uint32_t drain_bar = smem_addr(&sm.bars[14]);
 
   if (tid == 0) {
-    for (int k = 0; k < 23; ++k)  // scales: an arrival of each lane, and one for the notes
-      mbar_init(smem_addr(&sm.bars[k]),
-                k / 2 == kP || (k >= 16 && k < 20) ? 4 : k >= 12 && k < 16 ? 33 : 1);
+    // P: four warps; S: the products, every lane's copies of scales, and the notes
+    for (int k = 0; k < 15; ++k)
+      mbar_init(smem_addr(&sm.bars[k]), k / 2 == kP ? 4 : k / 2 == kS ? 34 : 1);
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
@@ -625,7 +598,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         const int flags = (w.first ? kFirst : 0) | (w.ends() || i + 1 == n ? kLast : 0) |
                           (first_tile == 0 && w.ends() ? kWhole : 0) |
                           (first_tile == 0 ? kSlot1 : 0) | (seg & 3) << kSeqShift;
-        if (i >= 4 && !warp_wait_bar(scale_free_bar(i), ((i - 4) >> 2) & 1)) break;
+        if (i >= 2 && !warp_wait(kS, i - 2)) break;
         // (a plain asynchronous copy: TMA takes about as long for 32 bytes as for a block of codes)
         const uint32_t dst = scale_dst + (i & 3) * (4 * kTile);
         if (cid >= 0)
@@ -633,10 +606,10 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         else
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
         __syncwarp();
-        copy_async_arrive(scale_bar(i));
+        copy_async_arrive(bar(kS, i & 1));
         if (lane == 0) {
           sm.meta[i & 3] = make_int4(flags, w.s, valid, 0);
-          mbar_arrive(scale_bar(i));
+          mbar_arrive(bar(kS, i & 1));
         }
         __syncwarp();
         // the query of the next sequence, whose buffer frees with the first product of this one
@@ -650,8 +623,8 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
         }
       }
       if (i < n && lane == 0)
-        for (int j = max(0, i - 3); j <= i; ++j)
-          mbar_wait_for(scale_bar(j), (j >> 2) & 1, kWaitLimitNs / 8);
+        for (int j = max(0, i - 1); j <= i; ++j)
+          mbar_wait_for(bar(kS, j & 1), (j >> 1) & 1, kWaitLimitNs / 8);
       __syncwarp();
       // rows of sequences without a context, dealt out over the ranges
       for (int s0 = r; s0 < P.num_seqs; s0 += 32 * P.ranges) {
@@ -670,83 +643,101 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     more_registers<kManyRegs>();
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
     // Sums of weights l and outputs acc are relative to a running reference, held as its negative
-    // nm.  A tile's product joins acc one iteration later, when P of the next tile is on its way,
-    // and a sequence's rows are written then too: nothing waits for a product just issued.
-    float acc[HN], l[HN], nm[HN], beta[HN];
+    // nm.  A tile's product joins acc one iteration later, and a sequence's rows are written when P
+    // of the next tile is on its way: nothing waits for a product just issued.
+    constexpr int HP = (HN + 1) / 2;
+    Pair acc[HP], l[HP], nm[HP], beta[HP];
     const float sign = P.scale_log2 < 0.f ? -1.f : 1.f;
     int before = 0, before_s = 0;  // flags and sequence of the tile before
     bool ok = true;
 #pragma unroll
-    for (int h = 0; h < HN; ++h) acc[h] = 0.f;
-    // every lane waits; whether all four warps go on is decided at the barriers below
-    auto wait_bar = [&](uint32_t at, int parity) -> bool {
-      const bool got = wait_phase(at, parity);
-      const bool all = __all_sync(0xffffffffu, got);
-      if (!all && lane == 0) fail();
-      return all;
-    };
-    auto wait = [&](int kind, int i) { return wait_bar(bar(kind, i & 1), (i >> 1) & 1); };
-    // acc += O(i) beta; behind a sequence's last tile its rows are written
+    for (int p = 0; p < HP; ++p) acc[p] = 0;
+    // (whether all four warps go on after a wait is decided at the barriers below)
+    // acc += O(i) beta.  The columns are read before P(i + 2) arrives, which lets another product
+    // overwrite them.
     auto add_output = [&](int i) {
       uint32_t o[COLS];
-      float v[HN];
+      Pair v[HP];
       tc_fence_after_sync();
       read_columns<COLS>(tm_o + lane_off + (i & 1) * NC, o);
       tc_fence_before_sync();
       join_terms<NT, HN>(o, v);
-      fma_heads(acc, v, beta, acc);
-      if (!(before & kLast)) return;
-      const int seq = before >> kSeqShift;
-      const float(*lsum)[kHeads] = sm.lsum[seq & 1];
-      const size_t idx =
-          (static_cast<size_t>(r) * 2 + ((before & kSlot1) ? 1 : 0)) * P.num_q_heads + h0;
-      T* out = static_cast<T*>(P.out) + (static_cast<size_t>(before_s) * P.num_q_heads + h0) * D;
 #pragma unroll
-      for (int h = 0; h < HN; ++h) {
-        if (h < hc) {
-          const float den = (lsum[0][h] + lsum[1][h]) + (lsum[2][h] + lsum[3][h]);  // > 0, or NaN
-          if (before & kWhole) {
-            out[h * D + tid] = from_f32<T>(__fdividef(acc[h], den));
-          } else {
-            P.part_o[(idx + h) * D + tid] = acc[h];
-            if (tid == 0) P.part_ml[idx + h].y = den;
-          }
+      for (int p = 0; p < HP; ++p) acc[p] = fma2(v[p], beta[p], acc[p]);
+    };
+    // The rows of the sequence that ended with the tile before.
+    auto write_rows = [&]() {
+      const int seq = (before >> kSeqShift) & 1;
+      Pair den[HP];  // > 0, or NaN
+#pragma unroll
+      for (int p = 0; p < HP; ++p) {
+        auto part = [&](int w) { return *reinterpret_cast<const Pair*>(&sm.lsum[seq][w][2 * p]); };
+        den[p] = add2(add2(part(0), part(1)), add2(part(2), part(3)));
+      }
+      if (before & kWhole) {
+        T* out = static_cast<T*>(P.out) +
+                 (static_cast<size_t>(before_s) * P.num_q_heads + h0) * D + tid;
+#pragma unroll
+        for (int p = 0; p < HP; ++p) {
+          float a0, a1, d0, d1;
+          split(acc[p], a0, a1);
+          split(den[p], d0, d1);
+          if (2 * p < hc) out[2 * p * D] = from_f32<T>(__fdividef(a0, d0));
+          if (2 * p + 1 < hc) out[(2 * p + 1) * D] = from_f32<T>(__fdividef(a1, d1));
+          acc[p] = 0;
         }
-        acc[h] = 0.f;
+      } else {
+        const size_t idx =
+            (static_cast<size_t>(r) * 2 + ((before & kSlot1) ? 1 : 0)) * P.num_q_heads + h0;
+        float* part = P.part_o + idx * D + tid;
+#pragma unroll
+        for (int p = 0; p < HP; ++p) {
+          float a0, a1, d0, d1;
+          split(acc[p], a0, a1);
+          split(den[p], d0, d1);
+          if (2 * p < hc) part[2 * p * D] = a0;
+          if (2 * p + 1 < hc) part[(2 * p + 1) * D] = a1;
+          if (tid == 0 && 2 * p < hc) P.part_ml[idx + 2 * p].y = d0;
+          if (tid == 0 && 2 * p + 1 < hc) P.part_ml[idx + 2 * p + 1].y = d1;
+          acc[p] = 0;
+        }
       }
     };
     for (int i = 0; i < n; ++i) {
       const int b = i & 1;
-      ok = ok && wait_bar(scale_bar(i), (i >> 2) & 1);
+      ok = ok && warp_wait(kS, i);
       const int4 meta = sm.meta[i & 3];
       const int flags = meta.x;
       const __nv_bfloat16* sc = scales + (i & 3) * 2 * kTile + tid;
       const float ks = __bfloat162float(sc[0]) * sign;
       float vs = __bfloat162float(sc[kTile]);
-      ok = ok && wait(kS, i);
       // scores but for the head's factor f > 0, which the exponent below applies
-      float x[HN];
+      Pair x[HP];
+      float xs[2 * HP];  // their halves
       if (ok) {
         uint32_t sr[COLS];
         tc_fence_after_sync();
         read_columns<COLS>(tm_s + lane_off + b * NC, sr);
         tc_fence_before_sync();
         join_terms<NT, HN>(sr, x);
-        mul_heads(x, x, ks);
+#pragma unroll
+        for (int p = 0; p < HP; ++p) x[p] = mul2(x[p], pair(ks, ks));
       } else {
 #pragma unroll
-        for (int h = 0; h < HN; ++h) x[h] = 0.f;
+        for (int p = 0; p < HP; ++p) x[p] = 0;
       }
       if (meta.z < kTile && tid >= meta.z) {  // past the context
         vs = 0.f;
 #pragma unroll
-        for (int h = 0; h < HN; ++h) x[h] = -INFINITY;
+        for (int p = 0; p < HP; ++p) x[p] = pair(-INFINITY, -INFINITY);
       }
+#pragma unroll
+      for (int p = 0; p < HP; ++p) split(x[p], xs[2 * p], xs[2 * p + 1]);
       // the tile's largest score of each head and largest |V scale|
       {
         float t[HN];
 #pragma unroll
-        for (int h = 0; h < HN; ++h) t[h] = redux_max(x[h]);
+        for (int h = 0; h < HN; ++h) t[h] = redux_max(xs[h]);
         const uint32_t tv = redux_max(__float_as_uint(vs) & 0x7fffffffu);
         if (lane == 0) {
 #pragma unroll
@@ -754,81 +745,107 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
           sm.vtop[b][warp] = tv;
         }
       }
+      // the product of the tile before (it has read the buffer of the weights); beta is that tile's
+      if (i > 0 && (ok = ok && warp_wait(kO, i - 1))) add_output(i - 1);
       ok = softmax_sync_and(ok);
       if (!ok) break;
       // (the query's factors are in place: they were written before the first tile's notes)
-      float f[HN], nt[HN], d[HN];  // nt: the tile's reference in log2 units, negated
-#pragma unroll
-      for (int h = 0; h < HN; ++h) {
-        f[h] = sm.f[flags >> kSeqShift][1][h];
-        nt[h] = fmaxf(max3(sm.top[b][0][h], sm.top[b][1][h], sm.top[b][2][h]), sm.top[b][3][h]);
-      }
+      const int seq = flags >> kSeqShift;
+      Pair nt[HP], d[HP];  // nt: the tile's reference in log2 units, negated
+      float most = -INFINITY;
       const uint32_t tv = max(max(sm.vtop[b][0], sm.vtop[b][1]), max(sm.vtop[b][2], sm.vtop[b][3]));
+#pragma unroll
+      for (int p = 0; p < HP; ++p) {
+        const int h = 2 * p;
+        auto top = [&](int w) { return *reinterpret_cast<const float2*>(&sm.top[b][w][h]); };
+        const float2 t0 = top(0), t1 = top(1), t2 = top(2), t3 = top(3);
+        nt[p] = mul2(pair(fmaxf(max3(t0.x, t1.x, t2.x), t3.x), fmaxf(max3(t0.y, t1.y, t2.y), t3.y)),
+                     *reinterpret_cast<const Pair*>(&sm.f[seq][1][h]));
+      }
       // |vs| 2^(134 - E) < 256 for the exponent field E of the largest
       const int E = min(254, max(8, static_cast<int>(tv >> 23)));
       const float cv = tv >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : vs * pow2_bits(261 - E);
       const float back = pow2_bits(E - 7);
-      mul_heads(nt, nt, f);
       if (flags & kFirst) {
 #pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          nm[h] = nt[h];
-          l[h] = 0.f;
+        for (int p = 0; p < HP; ++p) {
+          nm[p] = nt[p];
+          l[p] = 0;
         }
       }
-      fma_heads(d, nt, -1.f, nm);  // how far the tile's reference exceeds the running one
-      float most = d[0];
+      // how far the tile's reference exceeds the running one
 #pragma unroll
-      for (int h = 1; h < HN; ++h) most = fmaxf(most, d[h]);
+      for (int p = 0; p < HP; ++p) {
+        d[p] = fma2(nt[p], pair(-1.f, -1.f), nm[p]);
+        float lo, hi;
+        split(d[p], lo, hi);
+        most = HN == 1 ? lo : max3(most, lo, hi);
+      }
       if (most > 64.f) {  // the running reference moves
 #pragma unroll
-        for (int h = 0; h < HN; ++h) {
-          const float nn = fminf(nm[h], nt[h]);
-          const float a = fast_exp2(nn - nm[h]);
-          acc[h] *= a;
-          l[h] *= a;
-          beta[h] *= a;
-          nm[h] = nn;
-          d[h] = nn - nt[h];
+        for (int p = 0; p < HP; ++p) {
+          float n0, n1, t0, t1;
+          split(nm[p], n0, n1);
+          split(nt[p], t0, t1);
+          const float m0 = fminf(n0, t0), m1 = fminf(n1, t1);
+          const Pair a = pair(fast_exp2(m0 - n0), fast_exp2(m1 - n1));
+          acc[p] = mul2(acc[p], a);
+          l[p] = mul2(l[p], a);
+          nm[p] = pair(m0, m1);
+          d[p] = pair(m0 - t0, m1 - t1);
         }
       }
+      uint32_t w[HP];  // the weights times the V scale, as fp16 pairs
 #pragma unroll
-      for (int h = 0; h < HN; ++h) f[h] = sm.f[flags >> kSeqShift][0][h];
-      fma_heads(x, x, f, nt);
-      float w[HN];
-#pragma unroll
-      for (int h = 0; h < HN; ++h) {
-        d[h] = fast_exp2(d[h]);  // from the tile's reference to the running one
-        x[h] = fast_exp2(x[h]);
+      for (int p = 0; p < HP; ++p) {
+        float lo, hi;
+        split(d[p], lo, hi);
+        d[p] = pair(fast_exp2(lo), HN == 1 ? 0.f : fast_exp2(hi));  // to the running reference
+        split(fma2(x[p], *reinterpret_cast<const Pair*>(&sm.f[seq][0][2 * p]), nt[p]), lo, hi);
+        const Pair e = pair(fast_exp2(lo), HN == 1 ? 0.f : fast_exp2(hi));
+        l[p] = fma2(e, d[p], l[p]);
+        split(mul2(e, pair(cv, cv)), lo, hi);
+        w[p] = Mma<__half>::pack(lo, HN == 1 ? 0.f : hi);
       }
-      fma_heads(l, x, d, l);
-      mul_heads(w, x, cv);
-      // O(i - 1) has read the buffer of the weights
-      if (i > 0) ok = wait(kO, i - 1);
       // the weights' E4M3 terms: byte term * HN + head of the token's row
       {
-        uint32_t row[NC / 4];
+        uint32_t code[NT][HP];
 #pragma unroll
-        for (int k = 0; k < NC / 4; ++k) row[k] = 0u;
+        for (int q = 0; q < NT; ++q)
 #pragma unroll
-        for (int h = 0; h < HN; h += 2) {
-          uint32_t a = Mma<__half>::pack(w[h], h + 1 < HN ? w[h + 1] : 0.f);
-#pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            const uint32_t code = f16x2_to_e4m3x2(a);
-            const int at = q * HN + h;
-            if constexpr (HN == 1)
-              row[at >> 2] |= (code & 0xffu) << (8 * (at & 3));
-            else
-              row[at >> 2] |= code << (8 * (at & 3));
+          for (int p = 0; p < HP; ++p) {
+            code[q][p] = f16x2_to_e4m3x2(w[p]);
             if (q + 1 < NT) {
-              const uint32_t back2 = e4m3x2_to_f16x2(code);
-              const __half2 rest = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a),
-                                                   *reinterpret_cast<const __half2*>(&back2)),
+              const uint32_t got = e4m3x2_to_f16x2(code[q][p]);
+              const __half2 rest = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w[p]),
+                                                   *reinterpret_cast<const __half2*>(&got)),
                                            __float2half2_rn(16.f));
-              a = *reinterpret_cast<const uint32_t*>(&rest);
+              w[p] = *reinterpret_cast<const uint32_t*>(&rest);
             }
           }
+        uint32_t row[NC / 4];
+        if constexpr (HN >= 4) {
+#pragma unroll
+          for (int k = 0; k < NC / 4; ++k) {
+            const int q = 4 * k / HN, p = (4 * k - q * HN) / 2;
+            row[k] = q < NT ? __byte_perm(code[q < NT ? q : 0][p], code[q < NT ? q : 0][p + 1], 0x5410)
+                            : 0u;
+          }
+        } else {
+          uint32_t first = 0;  // all terms fit 8 bytes
+          uint32_t second = 0;
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            const uint32_t bits = HN == 1 ? code[q][0] & 0xffu : code[q][0];
+            const int at = q * HN;
+            if (at < 4)
+              first |= bits << (8 * at);
+            else
+              second |= bits << (8 * (at - 4));
+          }
+          row[0] = first;
+          row[1] = second;
+          row[2] = row[3] = 0u;
         }
 #pragma unroll
         for (int half = 0; half < NC / 16; ++half)
@@ -838,24 +855,27 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kP, b));
-        mbar_arrive(scale_free_bar(i));
-      }
-      // the tile before, while the tensor cores work on this one; its O is read before P(i + 1)
-      // arrives, which lets O(i + 1) overwrite it.  (beta is that tile's still.)
-      if (i > 0 && ok) add_output(i - 1);
-      mul_heads(beta, d, back);
+      if (lane == 0) mbar_arrive(bar(kP, b));
+      if (before & kLast) write_rows();  // while the tensor cores work on this tile
+#pragma unroll
+      for (int p = 0; p < HP; ++p) beta[p] = mul2(d[p], pair(back, back));
       if (flags & kLast) {
-        const float sum = reduce_heads(l, [](float p, float q) { return p + q; });
-        if (lane % (32 / HN) == 0)
-          sm.lsum[(flags >> kSeqShift) & 1][warp][lane / (32 / HN)] = sum;
+        float ls[2 * HP], some[HN];
+#pragma unroll
+        for (int p = 0; p < HP; ++p) split(l[p], ls[2 * p], ls[2 * p + 1]);
+#pragma unroll
+        for (int h = 0; h < HN; ++h) some[h] = ls[h];
+        const float sum = reduce_heads(some, [](float p, float q) { return p + q; });
+        if (lane % (32 / HN) == 0) sm.lsum[seq & 1][warp][lane / (32 / HN)] = sum;
         if (!(flags & kWhole) && tid == 0) {
           const size_t idx =
               (static_cast<size_t>(r) * 2 + ((flags & kSlot1) ? 1 : 0)) * P.num_q_heads + h0;
 #pragma unroll
-          for (int h = 0; h < HN; ++h)
-            if (h < hc) P.part_ml[idx + h].x = -nm[h];
+          for (int h = 0; h < HN; ++h) {
+            float both[2];
+            split(nm[h / 2], both[0], both[1]);
+            if (h < hc) P.part_ml[idx + h].x = -both[h & 1];
+          }
         }
       }
       before = flags;
@@ -863,9 +883,9 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       // (a wait that ran out shows at the next barrier)
     }
     if (n > 0) {  // the last tile; every warp comes to this barrier
-      ok = ok && wait(kO, n - 1);
+      if ((ok = ok && warp_wait(kO, n - 1))) add_output(n - 1);
       ok = softmax_sync_and(ok);
-      if (ok) add_output(n - 1);
+      if (ok) write_rows();  // (a range's last tile ends its sequence's part)
     }
     tc_fence_before_sync();
   }
