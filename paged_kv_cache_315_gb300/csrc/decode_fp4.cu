@@ -343,12 +343,21 @@ constexpr int kMergeWarps = 4;
 
 // One CTA per (range, query head): if a sequence begins in the range and goes on past it,
 // its partials are slot 1 of this range and slot 0 of every later range up to the last that
-// holds tiles of it.  Warp w takes partials w, w + 4, ...:
+// holds tiles of it:
 //   M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+// The threads first turn the (m, l) into weights; then warp w adds partials w, w + 4, ..., whose
+// loads depend on nothing any more, eight at a time: a single sequence may have a partial in each
+// of 456 ranges.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const Fp4Params P) {
   constexpr int V = D / 32;
-  __shared__ float red[kMergeWarps];
+  constexpr int kThreads = 32 * kMergeWarps;
+  constexpr int kOwn = (kRangeCtas + kThreads - 1) / kThreads;
+  using Vec = typename std::conditional<V == 1, float,
+                                        typename std::conditional<V == 2, float2, float4>::type>::type;
+  constexpr int kVecs = V * sizeof(float) / sizeof(Vec);
+  __shared__ float red[2][kMergeWarps];
+  __shared__ float weight[kRangeCtas];
   __shared__ float o_s[kMergeWarps][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = blockIdx.x, head = blockIdx.y;
@@ -362,37 +371,56 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const Fp4Pa
   auto index = [&](int p) {
     return (static_cast<size_t>(r + p) * 2 + (p == 0 ? 1 : 0)) * P.num_q_heads + head;
   };
+  float2 ml[kOwn];
   float M = -INFINITY;
-  for (int p = tid; p < np; p += 32 * kMergeWarps) M = fmaxf(M, __ldcg(&P.part_ml[index(p)]).x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, red[w]);
-  __syncthreads();
-  float acc[V], den = 0.f;
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < np; p += kMergeWarps) {
-    const size_t idx = index(p);
-    const float2 ml = __ldcg(&P.part_ml[idx]);
-    const float w = exp2f(ml.x - M);
-    den = fmaf(w, ml.y, den);
-    const float* src = P.part_o + idx * D + lane * V;
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, __ldcg(src + k), acc[k]);
+  for (int k = 0; k < kOwn; ++k) {
+    const int p = tid + k * kThreads;
+    ml[k] = p < np ? __ldcg(&P.part_ml[index(p)]) : make_float2(-INFINITY, 0.f);
   }
 #pragma unroll
-  for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = acc[k];
-  if (lane == 0) red[warp] = den;
+  for (int k = 0; k < kOwn; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, red[0][w]);
+  float den = 0.f;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int p = tid + k * kThreads;
+    if (p < np) {
+      const float w = exp2f(ml[k].x - M);
+      weight[p] = w;
+      den = fmaf(w, ml[k].y, den);
+    }
+  }
+  den = warp_sum(den);
+  if (lane == 0) red[1][warp] = den;
+  __syncthreads();
+  float acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 8
+  for (int p = warp; p < np; p += kMergeWarps) {
+    const Vec* src = reinterpret_cast<const Vec*>(P.part_o + index(p) * D) + lane;
+    const float w = weight[p];
+    Vec x[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) x[k] = __ldcg(src + 32 * k);
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, reinterpret_cast<const float*>(x)[k], acc[k]);
+  }
+  constexpr int kWide = V / kVecs;
+#pragma unroll
+  for (int k = 0; k < V; ++k) o_s[warp][(k / kWide * 32 + lane) * kWide + k % kWide] = acc[k];
   __syncthreads();
   den = 0.f;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) den += red[w];
+  for (int w = 0; w < kMergeWarps; ++w) den += red[1][w];
   T* out = static_cast<T*>(P.out) + (static_cast<size_t>(info.x) * P.num_q_heads + head) * D;
-  for (int d = tid; d < D; d += 32 * kMergeWarps) {
+  for (int d = tid; d < D; d += kThreads) {
     float num = 0.f;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) num += o_s[w][d];

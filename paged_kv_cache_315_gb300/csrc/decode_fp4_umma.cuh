@@ -53,6 +53,7 @@
 
 constexpr int kUTileBytes = kTile * 128;  // a K or V tile in shared memory (64 of 128 bytes data)
 constexpr int kUThreads = 256;
+constexpr int kTries = 1 << 18;  // of a wait: a second, at the 4 us that hardware holds each
 constexpr int kUScaleBytes = 4 * 2 * kTile * 2;  // [4 slots][K, V][128 tokens] bf16
 
 // Terms of a 16-bit number, and the columns of S and O: term * HN + head, padded to an N that
@@ -245,17 +246,15 @@ __device__ __forceinline__ void join_terms(const uint32_t (&r)[NT * HN], Pair (&
   }
 }
 
-// Waits for the phase of `bar` with the given parity, at most kWaitLimitNs.  The plain try_wait
-// is one instruction in which the hardware holds the thread for a while (given a time to hold it
-// becomes a loop of its own, with sleeps and clock reads).
+// Waits for the phase of `bar` with the given parity; false when that takes more than kTries tries.
+// The plain try_wait is one instruction in which the hardware holds the thread for a while (given a
+// time to hold it becomes a loop of its own, with sleeps and clock reads).  A limit on tries rather
+// than on time keeps the loop small: five roles' code shares an SM's instruction caches, and with
+// clock reads at every wait the kernel was 1-3% slower.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
-  do {
 #pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-  } while (global_timer_ns() - t0 < kWaitLimitNs);
+  for (int i = 0; i < kTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 
@@ -407,15 +406,14 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
   const int n = sp.tiles;
   const uint32_t tm_s = sm.tmem, tm_o = tm_s + 2 * NC;
 
-  // A wait ran out (the call's output is void): the warp ends its role, and the others' waits for
-  // it run out in turn.
-  auto fail = [&]() { raise_error(P.err, PKV_DERR_TIMEOUT); };
-  // A whole warp's wait for tile i's use of a two-slot barrier; false when it ran out.
+  // A whole warp's wait; false when it ran out (the call's output is void): the warp ends its role,
+  // and the others' waits for it run out in turn.
+  bool failed = false;
   auto warp_wait_bar = [&](uint32_t at, uint32_t parity) -> bool {
-    const bool ok = __all_sync(0xffffffffu, wait_phase(at, parity));
-    if (!ok && lane == 0) fail();
-    return ok;
+    failed = !__all_sync(0xffffffffu, wait_phase(at, parity));
+    return !failed;
   };
+  // The same for tile i's use of a two-slot barrier.
   auto warp_wait = [&](int kind, int i) {
     return warp_wait_bar(bar(kind, i & 1), (i >> 1) & 1);
   };
@@ -507,7 +505,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
       // every product is complete before tensor memory is released
       if (elect_one()) {
         umma_commit(drain_bar);
-        if (!mbar_wait_bounded(drain_bar, 0)) fail();
+        failed = !mbar_wait_bounded(drain_bar, 0) || failed;
       }
     } else {
       // ---- scales, notes, queries -----------------------------------------------------------
@@ -889,6 +887,7 @@ __global__ void __launch_bounds__(kUThreads, u_cols(u_terms<T>(), HN) == 16 ? 3 
     }
     tc_fence_before_sync();
   }
+  if (failed) raise_error(P.err, PKV_DERR_TIMEOUT);
   __syncthreads();
   if (warp == 5) {
     tc_fence_after_sync();
