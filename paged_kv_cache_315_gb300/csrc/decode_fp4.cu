@@ -30,7 +30,8 @@ namespace {
 
 constexpr int kTile = 128;       // tokens of a tile
 constexpr int kHeads = 8;        // query heads of a unit, at most
-constexpr int kRangeCtas = 456;  // CTAs the ranges aim for: three on each of 152 SMs
+constexpr int kRangeCtas = 456;  // CTAs the ranges aim for: three on each of 152 SMs,
+constexpr int kMaxRanges = 912;  // or six of the CUDA-core kernel's
 constexpr int kSimtWarps = 4;
 constexpr int kSimtThreads = 32 * kSimtWarps;
 
@@ -211,101 +212,134 @@ __device__ __forceinline__ float warp_sum(float v) {
 // CUDA-core path: any type, head_dim 32, 64, 128 or 256, any block size
 // ------------------------------------------------------------------------------------------
 //
-// Warp w takes tokens w, w + 4, ... of a segment; a lane holds head_dim / 32 neighbouring
-// elements of the row and of each query head, and a dot product ends in a warp sum.
+// A lane holds head_dim / 32 neighbouring elements of each row and of each query head.  A warp takes
+// U tokens at a time, whose rows it loads together; their U HN dot products (at most 32) are summed
+// over the lanes by one exchange that leaves each lane with the score of one (token, head), so the
+// softmax of all of them takes one exponential per lane, and the weights go back by broadcasts.
+// The loads in flight bound it (U rows of head_dim / 2 bytes per warp), then the exchanges.
 
+constexpr int simt_tokens(int HN) { return HN == 8 ? 4 : 8; }
+
+// A lane's E codes of a row, in the low bits.
 template <int E>
-__device__ __forceinline__ void load_codes(const uint8_t* row, int lane, float (&x)[E]) {
-  uint32_t w;
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* row, int lane) {
   if constexpr (E == 1)
-    w = __ldg(row + (lane >> 1)) >> (4 * (lane & 1));
+    return __ldg(row + (lane >> 1)) >> (4 * (lane & 1));
   else if constexpr (E == 2)
-    w = __ldg(row + lane);
+    return __ldg(row + lane);
   else if constexpr (E == 4)
-    w = __ldg(reinterpret_cast<const uint16_t*>(row) + lane);
+    return __ldg(reinterpret_cast<const uint16_t*>(row) + lane);
   else
-    w = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
-  float all[8];
-  decode8(w, 1.f, all);
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = all[e];
+    return __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
 }
 
-template <typename T, int E>
+template <typename T, int E, int HN>
 __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4Params P) {
   constexpr int D = 32 * E;
-  __shared__ float o_s[kSimtWarps][kHeads][D];
-  __shared__ float2 ml_s[kSimtWarps][kHeads];
+  constexpr int U = simt_tokens(HN), N = U * HN;
+  constexpr int G = 32 / N;  // lanes that hold the same (head, token)
+  __shared__ float o_s[kSimtWarps][HN][D];
+  __shared__ float2 ml_s[kSimtWarps][HN];
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int own_u = lane / G % U, own_h = lane / (G * U);
   const int units = P.num_kv_heads * P.num_chunks;
-  const int r = blockIdx.x / units, u = blockIdx.x - r * units;
-  const int g = u / P.num_chunks, c = u - g * P.num_chunks;
+  const int r = blockIdx.x / units, u0 = blockIdx.x - r * units;
+  const int g = u0 / P.num_chunks, c = u0 - g * P.num_chunks;
   const int h0 = g * P.group + c * P.chunk, hc = min(P.chunk, P.group - c * P.chunk);
   const int BS = P.block_size;
   griddep_wait();
-  const Span sp = find_span<kSimtThreads>(P, r, u == 0, nullptr);
+  const Span sp = find_span<kSimtThreads>(P, r, u0 == 0, nullptr);
   zero_empty_rows<T>(P, D, r, h0, hc, tid, kSimtThreads);
 
   int s = sp.s, tile = sp.tile, left = sp.tiles;
   while (left > 0) {
     const Segment seg = next_segment(P, s, tile, left);
-    float qr[kHeads][E], acc[kHeads][E], m[kHeads], l[kHeads];
+    float qr[HN][E], acc[HN][E];
     const T* qs = static_cast<const T*>(P.q) +
                   (static_cast<size_t>(seg.s) * P.num_q_heads + h0) * D + lane * E;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+    for (int h = 0; h < HN; ++h) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         qr[h][e] = h < hc ? to_f32(qs[h * D + e]) : 0.f;
         acc[h][e] = 0.f;
       }
     }
+    float m = -INFINITY, l = 0.f;  // of head own_h; l over this lane's tokens alone
     const int32_t* bt = P.block_tables + static_cast<size_t>(seg.s) * P.max_blocks_per_seq;
-    for (int t = seg.t0 + warp; t < seg.t1; t += kSimtWarps) {
-      const int j = t / BS, off = t - j * BS;
-      const int id = __ldg(&bt[j]);
-      float kf[E], vf[E], ks = 0.f, vs = 0.f;
-      if (id >= 0 && id < P.num_blocks) {
-        const size_t row = (static_cast<size_t>(id) * BS + off) * P.num_kv_heads + g;
-        const size_t at = (static_cast<size_t>(id) * P.num_kv_heads + g) * BS + off;
-        load_codes<E>(P.k_cache + row * (D / 2), lane, kf);
-        load_codes<E>(P.v_cache + row * (D / 2), lane, vf);
-        ks = __bfloat162float(P.k_scales[at]);
-        vs = __bfloat162float(P.v_scales[at]);
-      } else {  // reads as zeros
-        if (lane == 0) raise_error(P.err, PKV_DERR_BLOCK_ID);
+    for (int tb = seg.t0 + warp * U; tb < seg.t1; tb += kSimtWarps * U) {
+      int id[U];
 #pragma unroll
-        for (int e = 0; e < E; ++e) kf[e] = vf[e] = 0.f;
+      for (int u = 0; u < U; ++u) id[u] = tb + u < seg.t1 ? __ldg(&bt[(tb + u) / BS]) : -1;
+      uint32_t kw[U], vw[U];
+      float ks = 0.f, vs = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u, off = t - t / BS * BS;
+        kw[u] = vw[u] = 0;
+        if (id[u] >= 0 && id[u] < P.num_blocks) {
+          const size_t row = (static_cast<size_t>(id[u]) * BS + off) * P.num_kv_heads + g;
+          kw[u] = load_codes<E>(P.k_cache + row * (D / 2), lane);
+          vw[u] = load_codes<E>(P.v_cache + row * (D / 2), lane);
+          if (u == own_u) {
+            const size_t at = (static_cast<size_t>(id[u]) * P.num_kv_heads + g) * BS + off;
+            ks = __bfloat162float(P.k_scales[at]);
+            vs = __bfloat162float(P.v_scales[at]);
+          }
+        } else if (t < seg.t1 && lane == 0) {  // reads as zeros
+          raise_error(P.err, PKV_DERR_BLOCK_ID);
+        }
       }
-      const float f = ks * P.scale_log2;
+      float dot[N];
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        if (h < hc) {
-          float dot = 0.f;
+      for (int u = 0; u < U; ++u) {
+        float kf[8];
+        decode8(kw[u], 1.f, kf);
 #pragma unroll
-          for (int e = 0; e < E; ++e) dot = fmaf(qr[h][e], kf[e], dot);
-          const float sl = warp_sum(dot) * f;
-          const float mn = fmaxf(m[h], sl);
-          const float a = exp2f(m[h] - mn), p = exp2f(sl - mn);
-          l[h] = l[h] * a + p;
-          const float pv = p * vs;
+        for (int h = 0; h < HN; ++h) {
+          float d = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(pv, vf[e], acc[h][e] * a);
-          m[h] = mn;
+          for (int e = 0; e < E; ++e) d = fmaf(qr[h][e], kf[e], d);
+          dot[h * U + u] = d;
+        }
+      }
+      const bool live = tb + own_u < seg.t1;
+      const float sum = reduce_heads(dot, [](float x, float y) { return x + y; });
+      const float sl = live ? sum * (ks * P.scale_log2) : -INFINITY;
+      float mn = sl;
+#pragma unroll
+      for (int o = G; o < G * U; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mn = fmaxf(m, mn);
+      const float a = exp2f(m - mn), p = live ? exp2f(sl - mn) : 0.f;
+      m = mn;
+      l = fmaf(l, a, p);
+      const float pv = p * vs;
+#pragma unroll
+      for (int h = 0; h < HN; ++h) {
+        const float ah = __shfl_sync(0xffffffffu, a, h * U * G);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[h][e] *= ah;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float vf[8];
+        decode8(vw[u], 1.f, vf);
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          const float w = __shfl_sync(0xffffffffu, pv, (h * U + u) * G);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(w, vf[e], acc[h][e]);
         }
       }
     }
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      if (h < hc) {
+    for (int o = G; o < G * U; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane % (G * U) == 0) ml_s[warp][own_h] = make_float2(m, l);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o_s[warp][h][lane * E + e] = acc[h][e];
-        if (lane == 0) ml_s[warp][h] = make_float2(m[h], l[h]);
-      }
-    }
+    for (int h = 0; h < HN; ++h)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o_s[warp][h][lane * E + e] = acc[h][e];
     __syncthreads();
     for (int i = tid; i < hc * D; i += kSimtThreads) {
       const int h = i / D, d = i - h * D;
@@ -347,17 +381,18 @@ constexpr int kMergeWarps = 4;
 //   M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 // The threads first turn the (m, l) into weights; then warp w adds partials w, w + 4, ..., whose
 // loads depend on nothing any more, eight at a time: a single sequence may have a partial in each
-// of 456 ranges.
+// range (131072 tokens, one KV head, 456 partials: 37 us a call with loads four at a time behind
+// their weights, 31 like this).
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const Fp4Params P) {
   constexpr int V = D / 32;
   constexpr int kThreads = 32 * kMergeWarps;
-  constexpr int kOwn = (kRangeCtas + kThreads - 1) / kThreads;
+  constexpr int kOwn = (kMaxRanges + kThreads - 1) / kThreads;
   using Vec = typename std::conditional<V == 1, float,
                                         typename std::conditional<V == 2, float2, float4>::type>::type;
   constexpr int kVecs = V * sizeof(float) / sizeof(Vec);
   __shared__ float red[2][kMergeWarps];
-  __shared__ float weight[kRangeCtas];
+  __shared__ float weight[kMaxRanges];
   __shared__ float o_s[kMergeWarps][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = blockIdx.x, head = blockIdx.y;
@@ -439,6 +474,13 @@ struct Fp4Layout {
   size_t o_offset, ml_offset, info_offset, total;
 };
 
+// Block sizes that the tensor-core kernel's copies serve: they divide a tile, and a block of one KV
+// head is 8 rows of shared memory or more.
+bool umma_shape(int head_dim, int block_size) {
+  return head_dim == 128 && (block_size == 8 || block_size == 16 || block_size == 32 ||
+                             block_size == 64 || block_size == 128);
+}
+
 Fp4Layout layout(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                  int max_blocks_per_seq) {
   Fp4Layout w{};
@@ -449,7 +491,8 @@ Fp4Layout layout(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, 
   const long long tiles =
       static_cast<long long>(num_seqs) *
       ((static_cast<long long>(max_blocks_per_seq) * block_size + kTile - 1) / kTile);
-  w.ranges = static_cast<int>(std::max(1LL, std::min(kRangeCtas / units, tiles)));
+  const long long ctas = umma_shape(head_dim, block_size) ? kRangeCtas : kMaxRanges;
+  w.ranges = static_cast<int>(std::max(1LL, std::min(ctas / units, tiles)));
   if (w.ranges <= 1) return w;
   const size_t rows = static_cast<size_t>(w.ranges) * 2 * num_q_heads;
   w.ml_offset = align_up(rows * head_dim * sizeof(float), 256);
@@ -507,23 +550,31 @@ UmmaFn umma_for(int chunk, int& smem) {
   }
 }
 
-// Whether the tensor-core kernel serves a call: TMA wants rows of whole 128-element boxes, a
-// block of 8 to 128 tokens that divides the tile, and 16-byte aligned scales.
+// Whether the tensor-core kernel serves a call.  Its products read 8-bit terms of 16-bit numbers,
+// and its copies of scales 16 bytes.  It is the faster one of the two at every size measured: 11 us
+// against 15 for one sequence of 100 tokens, 61 against 795 for 128 sequences of 128 to 8192 tokens
+// with 8 query heads per KV head.
 bool uses_umma(const DecodeFp4Args& a) {
-  return a.dtype != PKV_F32 && a.head_dim == 128 &&
-         (a.block_size == 8 || a.block_size == 16 || a.block_size == 32 || a.block_size == 64 ||
-          a.block_size == 128) &&
+  return a.dtype != PKV_F32 && umma_shape(a.head_dim, a.block_size) &&
          reinterpret_cast<uintptr_t>(a.k_scales) % 16 == 0 &&
          reinterpret_cast<uintptr_t>(a.v_scales) % 16 == 0;
 }
 
+template <typename T, int E>
+Fp4Fn simt_heads(int chunk) {
+  return chunk <= 1   ? decode_fp4_simt_kernel<T, E, 1>
+         : chunk <= 2 ? decode_fp4_simt_kernel<T, E, 2>
+         : chunk <= 4 ? decode_fp4_simt_kernel<T, E, 4>
+                      : decode_fp4_simt_kernel<T, E, 8>;
+}
+
 template <typename T>
-Fp4Fn simt_for(int D) {
+Fp4Fn simt_for(int D, int chunk) {
   switch (D) {
-    case 32: return decode_fp4_simt_kernel<T, 1>;
-    case 64: return decode_fp4_simt_kernel<T, 2>;
-    case 128: return decode_fp4_simt_kernel<T, 4>;
-    case 256: return decode_fp4_simt_kernel<T, 8>;
+    case 32: return simt_heads<T, 1>(chunk);
+    case 64: return simt_heads<T, 2>(chunk);
+    case 128: return simt_heads<T, 4>(chunk);
+    case 256: return simt_heads<T, 8>(chunk);
     default: return nullptr;
   }
 }
@@ -581,13 +632,18 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
   P.max_blocks_per_seq = a.max_blocks_per_seq;
   P.num_blocks = a.num_blocks;
   P.block_size = a.block_size;
-  P.ranges = w.ranges;
+  const bool umma = uses_umma(a);
+  // The variant that has two CTAs on an SM takes as many ranges as are resident at a time (128
+  // sequences of 2048 tokens, fp16, 8 query heads per KV head: 72 us, with half as many again 94).
+  P.ranges = umma && a.dtype == PKV_F16 && w.chunk > 4
+                 ? std::max(1, std::min(w.ranges, kRangeCtas * 2 / 3 / (a.num_kv_heads * w.num_chunks)))
+                 : w.ranges;
   P.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const long long grid = static_cast<long long>(w.ranges) * a.num_kv_heads * w.num_chunks;
-  if (grid > INT_MAX || (w.ranges > 1 && a.num_q_heads > 65535)) return PKV_EUNSUPPORTED;
-  const Fp4Fn fn = a.dtype == PKV_F32    ? simt_for<float>(a.head_dim)
-                   : a.dtype == PKV_BF16 ? simt_for<__nv_bfloat16>(a.head_dim)
-                                         : simt_for<__half>(a.head_dim);
+  const long long grid = static_cast<long long>(P.ranges) * a.num_kv_heads * w.num_chunks;
+  if (grid > INT_MAX || (P.ranges > 1 && a.num_q_heads > 65535)) return PKV_EUNSUPPORTED;
+  const Fp4Fn fn = a.dtype == PKV_F32    ? simt_for<float>(a.head_dim, w.chunk)
+                   : a.dtype == PKV_BF16 ? simt_for<__nv_bfloat16>(a.head_dim, w.chunk)
+                                         : simt_for<__half>(a.head_dim, w.chunk);
   const Fp4Fn merge = a.dtype == PKV_F32    ? merge_for<float>(a.head_dim)
                       : a.dtype == PKV_BF16 ? merge_for<__nv_bfloat16>(a.head_dim)
                                             : merge_for<__half>(a.head_dim);
@@ -602,7 +658,7 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  if (uses_umma(a)) {
+  if (umma) {
     CUtensorMap kmap, vmap;
     const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
     if (!make_codes_map(&kmap, a.k_cache, a.num_kv_heads, slots, a.block_size) ||
@@ -621,8 +677,8 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
     cfg.blockDim = dim3(kSimtThreads);
     if (cudaLaunchKernelEx(&cfg, fn, P) != cudaSuccess) return PKV_ECUDA;
   }
-  if (w.ranges > 1) {
-    cfg.gridDim = dim3(static_cast<unsigned>(w.ranges - 1), static_cast<unsigned>(a.num_q_heads));
+  if (P.ranges > 1) {
+    cfg.gridDim = dim3(static_cast<unsigned>(P.ranges - 1), static_cast<unsigned>(a.num_q_heads));
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, merge, P) != cudaSuccess) return PKV_ECUDA;

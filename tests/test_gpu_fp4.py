@@ -372,6 +372,51 @@ def test_decode_streams_and_graphs(pkv):
     c.check(outs[0])
 
 
+def test_decode_on_given_streams(pkv):
+    """The default stream by object and by handle, and a captured stream given by name."""
+    c = Case("bf16", 8, 2, 128, 16, [700, 1, 300, 2000], seed=8)
+    want = c.run(pkv)
+    torch.cuda.synchronize()
+    assert torch.equal(c.run(pkv, stream=torch.cuda.default_stream()), want)
+    assert torch.equal(c.run(pkv, stream=0), want)
+    q, args = c.q.cuda(), c.dev()
+    out = torch.full_like(q, 9.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        pkv.paged_attn_decode_fp4(out, q, *args, c.scale, stream=side)
+    for _ in range(3):
+        c.run(pkv)  # eager calls between the replays
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_decode_scales_off_16_bytes(pkv, dtype):
+    c = Case(dtype, 8, 2, 128, 16, [700, 1, 0, 300, 2000], seed=8)
+    args = c.dev()
+    for i in (2, 3):
+        flat = torch.empty(args[i].numel() + 1, dtype=torch.bfloat16, device="cuda")
+        flat[1:] = args[i].flatten()
+        args[i] = flat[1:].view(args[i].shape)
+        assert args[i].data_ptr() % 16 != 0
+    out = torch.full_like(c.q, 9.0, device="cuda")
+    pkv.paged_attn_decode_fp4(out, c.q.cuda(), *args, c.scale)
+    assert pkv.pkv_device_error() == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,bs", [("f16", 16, 2, 128, 16), ("bf16", 2, 1, 64, 16),
+                                               ("f32", 6, 1, 128, 32), ("bf16", 3, 1, 128, 16)])
+def test_decode_more_tiles_than_ranges(pkv, dtype, Hq, Hkv, D, bs):
+    c = Case(dtype, Hq, Hkv, D, bs, [60000, 17, 0, 70000, 129, 128], seed=21)
+    got = c.run(pkv)
+    assert pkv.pkv_device_error() == 0
+    c.check(got)
+
+
 # ---- together ---------------------------------------------------------------------------------
 
 

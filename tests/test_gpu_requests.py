@@ -185,3 +185,28 @@ def test_graph_replays_and_streams(pkv):
     with torch.cuda.stream(side):
         side.wait_stream(torch.cuda.default_stream())
         p.step(pkv, p.lens + 3, 3 * B)
+
+
+def test_many_rows_in_a_graph(pkv):
+    """More rows than one cluster takes: the two grids of that form, captured and replayed."""
+    B, bs, MB, rows = 300, 16, 40, 20000
+    p = Pool(B, MB, B * MB, 9, B * MB, bs, B * MB)
+    p.step(pkv, np.arange(B), rows)
+    target = torch.zeros(B, dtype=torch.int32, device="cuda")
+    slots = torch.empty(rows, dtype=torch.int64, device="cuda")
+    start = torch.empty(B + 1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.kv_resize_requests(p.dev["tables"], p.dev["lens"], target, p.dev["ring"],
+                               p.dev["pool"], slots, start, bs, p.num_blocks)
+    for delta in (60, -7, 70, 66, -500):  # 66: more than the rows
+        want_target = np.maximum(p.lens + delta, 0).astype(np.int32)
+        target.copy_(torch.from_numpy(want_target))
+        g.replay()
+        want, want_start, err = ref.resize(p.tables, p.lens, want_target, p.ring, p.pool, rows, bs,
+                                           p.num_blocks)
+        assert pkv.pkv_device_error() == err
+        assert np.array_equal(slots.cpu().numpy(), want)
+        assert np.array_equal(start.cpu().numpy(), want_start)
+        for k in ("ring", "pool", "tables", "lens"):
+            assert np.array_equal(p.dev[k].cpu().numpy(), getattr(p, k)), k
