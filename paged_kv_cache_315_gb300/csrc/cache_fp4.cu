@@ -53,24 +53,25 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[kElems]) {
   }
 }
 
-// The 8 codes (element 0 in the lowest four bits) of x / scale, the IEEE quotient.  With r the
-// correctly rounded reciprocal of the scale, y = x r and e = x - y scale (exact in one FMA), y + e r
-// is the correctly rounded quotient (Markstein, 1990): three operations an element where the
-// division takes some ten (and one for the sign, which a negative zero loses).  Scales near the ends of fp32's range, where e or r could leave it, take
-// the division.
+// The IEEE quotient x / d, given r, the correctly rounded reciprocal of d: with y = x r and
+// e = y d - x (exact in one FMA), y - e r is the correctly rounded quotient (Markstein, 1990), three
+// operations where the division takes some ten.  With e taken this way round a zero keeps its sign:
+// x = -0 gives y = -0, e = +0 and -0 r + y = -0.  Divisors near the ends of fp32's range, where e or
+// r could leave it, take the division.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float y = x * r, e = fmaf(y, d, -x);
+  return fmaf(-e, r, y);
+}
+
+// The 8 codes (element 0 in the lowest four bits) of x / scale.
 __device__ __forceinline__ uint32_t encode8(const float (&x)[kElems], float scale) {
   uint32_t word = 0;
-  const bool plain = scale > 0x1p-100f && scale < 0x1p100f;
-  if (plain) {
+  if (scale > 0x1p-100f && scale < 0x1p100f) {
     const float r = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y0 = x[2 * i] * r, y1 = x[2 * i + 1] * r;
-      const float e0 = fmaf(-y0, scale, x[2 * i]), e1 = fmaf(-y1, scale, x[2 * i + 1]);
-      word |= f32x2_to_e2m1x2(copysignf(fmaf(e0, r, y0), x[2 * i]),
-                              copysignf(fmaf(e1, r, y1), x[2 * i + 1]))
+    for (int i = 0; i < 4; ++i)
+      word |= f32x2_to_e2m1x2(quotient(x[2 * i], scale, r), quotient(x[2 * i + 1], scale, r))
               << (8 * i);
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -80,21 +81,29 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[kElems], float scal
   return word;
 }
 
+// The largest of three magnitudes, NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
 // A row of D elements is held by D / 8 lanes of a warp.  Returns its codes and, in `scale`,
 // its scale (the same in each of those lanes).
 template <int D>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[kElems], __nv_bfloat16& scale) {
-  // |x| as bits orders like |x|, and a NaN above infinity above every number
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kElems; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  // magnitudes' bits order like the magnitudes, and a NaN above infinity above every number
+  uint32_t top = __float_as_uint(max_abs(max_abs(x[0], x[1], x[2]), max_abs(x[3], x[4], x[5]),
+                                         max_abs(x[6], x[7], 0.f)));
 #pragma unroll
   for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top >= 0x7f800000u) {  // a NaN or an infinity in the row: every element reads as NaN
     scale = __ushort_as_bfloat16(0x7fff);
     return 0;
   }
-  scale = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 6.f));
+  const float amax = __uint_as_float(top);
+  scale = __float2bfloat16_rn(amax > 0x1p-100f ? quotient(amax, 6.f, 1.f / 6.f)
+                                               : __fdiv_rn(amax, 6.f));
   const float s = __bfloat162float(scale);
   return s > 0.f ? encode8(x, s) : 0u;
 }
