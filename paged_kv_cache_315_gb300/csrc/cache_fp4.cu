@@ -4,9 +4,10 @@
 // nearest to amax / 6 (6 is the largest E2M1 magnitude) and each element's code the E2M1
 // value nearest to x / scale, ties to the even code.  Both kernels are byte movement with a
 // little arithmetic: per element the write reads 2 bytes (16-bit types) and stores half a
-// byte, so the arithmetic per element has to stay within a few instructions for HBM to
-// remain the bound.
+// byte, and at the copy bandwidth of HBM an SM has 7 clocks for 128 of them, some 28 issue
+// slots, so what counts is the number of instructions per element.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "fp4.cuh"
@@ -16,8 +17,9 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;  // resident at 64 registers; the grids hold no more
-constexpr int kElems = 8;  // elements a lane holds of a row: 16 bytes of a 16-bit type
+constexpr int kWriteCtas = 4, kReadCtas = 5;  // on an SM; the grids hold no more than are resident
+constexpr int kElems = 8;        // elements of a run: 16 bytes of a 16-bit type
+constexpr int kLaneElems = 16;   // elements a lane holds of a row, in runs D / 2 (or D / 4) apart
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[kElems]) {
@@ -38,11 +40,11 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[kElems]) {
   }
 }
 
+// 16 bytes of values: 8 of a 16-bit type, or the first 4.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[kElems]) {
+__device__ __forceinline__ void store_run(T* p, const float (&x)[kElems]) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   } else {
     uint4 a;
     a.x = Mma<T>::pack(x[0], x[1]);
@@ -88,24 +90,28 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return r;
 }
 
-// A row of D elements is held by D / 8 lanes of a warp.  Returns its codes and, in `scale`,
-// its scale (the same in each of those lanes).
+// A row of D elements is held by D / 16 lanes of a warp, two runs of 8 in each.  Returns its codes
+// and, in `scale`, its scale (the same in each of those lanes).
 template <int D>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[kElems], __nv_bfloat16& scale) {
+__device__ __forceinline__ uint2 quantise(const float (&x)[2][kElems], __nv_bfloat16& scale) {
   // magnitudes' bits order like the magnitudes, and a NaN above infinity above every number
-  uint32_t top = __float_as_uint(max_abs(max_abs(x[0], x[1], x[2]), max_abs(x[3], x[4], x[5]),
-                                         max_abs(x[6], x[7], 0.f)));
+  float most[2];
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int c = 0; c < 2; ++c)
+    most[c] = max_abs(max_abs(x[c][0], x[c][1], x[c][2]), max_abs(x[c][3], x[c][4], x[c][5]),
+                      max_abs(x[c][6], x[c][7], 0.f));
+  uint32_t top = __float_as_uint(max_abs(most[0], most[1], 0.f));
+#pragma unroll
+  for (int o = D / 32; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top >= 0x7f800000u) {  // a NaN or an infinity in the row: every element reads as NaN
     scale = __ushort_as_bfloat16(0x7fff);
-    return 0;
+    return make_uint2(0, 0);
   }
   const float amax = __uint_as_float(top);
   scale = __float2bfloat16_rn(amax > 0x1p-100f ? quotient(amax, 6.f, 1.f / 6.f)
                                                : __fdiv_rn(amax, 6.f));
   const float s = __bfloat162float(scale);
-  return s > 0.f ? encode8(x, s) : 0u;
+  return s > 0.f ? make_uint2(encode8(x[0], s), encode8(x[1], s)) : make_uint2(0, 0);
 }
 
 // The (token, head) rows a group of lanes takes, `stride` rows apart, without a division in the
@@ -138,107 +144,100 @@ __device__ __forceinline__ size_t scale_at(uint32_t slot, int head, int num_head
          (slot - block * static_cast<uint32_t>(block_size));
 }
 
-// One group of D / 8 lanes per (token, head) row, its key and its value row together; kRows rows
-// are loaded before the first of them is worked on.
+// One group of D / 16 lanes per (token, head) row, its key and its value row together.  What bounds it
+// is the issue of some 80 instructions per lane and row: with 8 elements a lane instead of 16 the
+// exchanges, the scale and the addresses weigh twice as much (131072 x 8 bf16 rows: 174 us for 134).
+// Four CTAs of one row a lane hide the loads better than fewer with two (2 CTAs: 166 us, 3: 163), and
+// more of them lack registers (6: 157).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kWriteCtas)
     write_fp4_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ kc,
                      uint8_t* __restrict__ vc, __nv_bfloat16* __restrict__ ks,
                      __nv_bfloat16* __restrict__ vs, const int64_t* __restrict__ slots,
                      long long num_rows, int num_heads, int block_size, long long num_slots,
                      unsigned* err) {
-  constexpr int LPR = D / kElems;
-  constexpr int kRows = sizeof(T) == 4 ? 1 : 2;
+  constexpr int LPR = D / kLaneElems;
   const int sub = threadIdx.x % LPR;
   const long long stride = static_cast<long long>(gridDim.x) * (kThreads / LPR);
   RowWalk w(static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR, stride,
             num_heads);
   // every lane of a warp runs the same number of iterations: the shuffles are warp-wide
   for (long long base = static_cast<long long>(blockIdx.x) * (kThreads / LPR); base < num_rows;
-       base += kRows * stride) {
-    float xk[kRows][kElems], xv[kRows][kElems];
-    long long slot[kRows];
-    int head[kRows];
+       base += stride) {
+    const bool in = w.row < num_rows;
+    const long long r = in ? w.row : num_rows - 1;
+    const long long slot = in ? __ldg(&slots[w.token]) : -1;
+    const int head = w.head;
+    w.next(stride);
+    float xk[2][kElems], xv[2][kElems];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const bool in = w.row < num_rows;
-      const long long r = in ? w.row : num_rows - 1;
-      slot[u] = in ? __ldg(&slots[w.token]) : -1;
-      head[u] = w.head;
-      load8(k + r * D + sub * kElems, xk[u]);
-      load8(v + r * D + sub * kElems, xv[u]);
-      w.next(stride);
+    for (int c = 0; c < 2; ++c) {
+      load8(k + r * D + (c * LPR + sub) * kElems, xk[c]);
+      load8(v + r * D + (c * LPR + sub) * kElems, xv[c]);
     }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      __nv_bfloat16 sk, sv;
-      const uint32_t ck = quantise<D>(xk[u], sk), cv = quantise<D>(xv[u], sv);
-      if (slot[u] < 0) continue;  // padding, or past the last row
-      if (slot[u] >= num_slots) {
-        if (head[u] == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
-        continue;
-      }
-      const long long at = slot[u] * num_heads + head[u];
-      *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + sub * 4) = ck;
-      *reinterpret_cast<uint32_t*>(vc + at * (D / 2) + sub * 4) = cv;
-      if (sub == 0) {
-        const size_t place = scale_at(static_cast<uint32_t>(slot[u]), head[u], num_heads, block_size);
-        ks[place] = sk;
-        vs[place] = sv;
-      }
+    __nv_bfloat16 sk, sv;
+    const uint2 ck = quantise<D>(xk, sk), cv = quantise<D>(xv, sv);
+    if (slot < 0) continue;  // padding, or past the last row
+    if (slot >= num_slots) {
+      if (head == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
+      continue;
+    }
+    const long long at = slot * num_heads + head;
+    uint32_t* krow = reinterpret_cast<uint32_t*>(kc + at * (D / 2));
+    uint32_t* vrow = reinterpret_cast<uint32_t*>(vc + at * (D / 2));
+    krow[sub] = ck.x;
+    krow[LPR + sub] = ck.y;
+    vrow[sub] = cv.x;
+    vrow[LPR + sub] = cv.y;
+    if (sub == 0) {
+      const size_t place = scale_at(static_cast<uint32_t>(slot), head, num_heads, block_size);
+      ks[place] = sk;
+      vs[place] = sv;
     }
   }
 }
 
-// Four codes' bytes (8 elements) per thread and row; kRows rows of a thread are in flight together.
+// A lane takes 16 elements of a row in runs whose values are 16 bytes, so that neighbouring lanes'
+// stores lie side by side (fp32 rows with a lane's 32 bytes in a row: 274 us for 212).  HBM bounds
+// it: 131072 x 8 bf16 rows in 112 us, 6.0 TB/s.  Four CTAs that keep two rows of a lane in flight
+// take 116.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kReadCtas)
     read_fp4_kernel(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc,
                     const uint8_t* __restrict__ vc, const __nv_bfloat16* __restrict__ ks,
                     const __nv_bfloat16* __restrict__ vs, const int64_t* __restrict__ slots,
                     long long num_rows, int num_heads, int block_size, long long num_slots,
                     unsigned* err) {
-  constexpr int LPR = D / kElems;
-  constexpr int kRows = 4;
+  constexpr int LPR = D / kLaneElems;
+  constexpr int kRun = 16 / sizeof(T), kRuns = kLaneElems / kRun;
+  using Codes = typename std::conditional<kRun == 8, uint32_t, uint16_t>::type;
   const int sub = threadIdx.x % LPR;
   const long long stride = static_cast<long long>(gridDim.x) * (kThreads / LPR);
-  RowWalk w(static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR, stride,
-            num_heads);
-  while (w.row < num_rows) {
-    long long row[kRows], slot[kRows];
-    int head[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      row[u] = w.row;
-      head[u] = w.head;
-      slot[u] = w.row < num_rows ? __ldg(&slots[w.token]) : -1;
-      w.next(stride);
+  for (RowWalk w(static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR, stride,
+                 num_heads);
+       w.row < num_rows; w.next(stride)) {
+    const long long slot = __ldg(&slots[w.token]);
+    if (slot < 0) continue;  // padding
+    if (slot >= num_slots) {
+      if (w.head == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
+      continue;
     }
-    uint32_t ck[kRows], cv[kRows];
-    float sk[kRows], sv[kRows];
+    const long long at = slot * num_heads + w.head;
+    const size_t place = scale_at(static_cast<uint32_t>(slot), w.head, num_heads, block_size);
+    Codes ck[kRuns], cv[kRuns];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (slot[u] >= num_slots) {
-        if (head[u] == 0 && sub == 0) raise_error(err, PKV_DERR_SLOT);
-        slot[u] = -1;
-      }
-      if (slot[u] >= 0) {
-        const long long at = slot[u] * num_heads + head[u];
-        const size_t place = scale_at(static_cast<uint32_t>(slot[u]), head[u], num_heads, block_size);
-        ck[u] = __ldg(reinterpret_cast<const uint32_t*>(kc + at * (D / 2)) + sub);
-        cv[u] = __ldg(reinterpret_cast<const uint32_t*>(vc + at * (D / 2)) + sub);
-        sk[u] = __bfloat162float(ks[place]);
-        sv[u] = __bfloat162float(vs[place]);
-      }
+    for (int c = 0; c < kRuns; ++c) {
+      ck[c] = __ldg(reinterpret_cast<const Codes*>(kc + at * (D / 2)) + c * LPR + sub);
+      cv[c] = __ldg(reinterpret_cast<const Codes*>(vc + at * (D / 2)) + c * LPR + sub);
     }
+    const float sk = __bfloat162float(ks[place]), sv = __bfloat162float(vs[place]);
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (slot[u] < 0) continue;
+    for (int c = 0; c < kRuns; ++c) {
       float x[kElems];
-      decode8(ck[u], sk[u], x);
-      store8(k + row[u] * D + sub * kElems, x);
-      decode8(cv[u], sv[u], x);
-      store8(v + row[u] * D + sub * kElems, x);
+      decode8(ck[c], sk, x);
+      store_run(k + w.row * D + (c * LPR + sub) * kRun, x);
+      decode8(cv[c], sv, x);
+      store_run(v + w.row * D + (c * LPR + sub) * kRun, x);
     }
   }
 }
@@ -255,9 +254,10 @@ template <typename T, int D>
 int run(const CacheFp4Args& a, bool write, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.num_tokens) * a.num_kv_heads;
   const long long slots = static_cast<long long>(a.num_blocks) * a.block_size;
-  const long long per_cta = kThreads / (D / kElems);
-  const int grid = static_cast<int>(
-      std::max(1LL, std::min((rows + per_cta - 1) / per_cta, static_cast<long long>(kCtasPerSm) * sm_count())));
+  const long long per_cta = kThreads / (D / kLaneElems);
+  const long long resident = static_cast<long long>(write ? kWriteCtas : kReadCtas) * sm_count();
+  const int grid =
+      static_cast<int>(std::max(1LL, std::min((rows + per_cta - 1) / per_cta, resident)));
   uint8_t *kc = static_cast<uint8_t*>(a.k_cache), *vc = static_cast<uint8_t*>(a.v_cache);
   __nv_bfloat16 *ks = static_cast<__nv_bfloat16*>(a.k_scales),
                 *vs = static_cast<__nv_bfloat16*>(a.v_scales);
