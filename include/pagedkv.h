@@ -340,7 +340,9 @@ int kv_cache_write_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  * of zero.  A row that holds a NaN or an infinity gets a NaN scale and codes of zero: every
  * element of it reads as NaN.  k and v are [num_tokens, num_kv_heads, head_dim] in `dtype`
  * (any of the three types), 16-byte aligned.  Slot rules and return codes are those of
- * kv_cache_write (PKV_EUNSUPPORTED for another head_dim); equal inputs give equal codes.
+ * kv_cache_write (PKV_EUNSUPPORTED for another head_dim); equal inputs give equal codes.  Two tokens naming
+ * the same slot in one call leave that slot undefined: codes of one may meet the scale of the
+ * other.  num_blocks * block_size must be below 2^31 - 1 in all three calls (PKV_EINVAL).
  */
 int kv_cache_write_fp4(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scales,
                        void* v_scales, const int64_t* slot_mapping, int num_tokens,
@@ -377,6 +379,12 @@ int kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache
  * (and chunk of at most 8 query heads), whatever the lengths of the sequences; a sequence cut
  * by a range's end is merged by log-sum-exp in a second grid.  The result does not depend on
  * how the work happened to be scheduled: equal inputs give equal outputs.
+ *
+ * With head_dim 128, block_size 8, 16, 32, 64 or 128, q and out in 16 bits and scales aligned
+ * to 16 bytes, the products run on the tensor cores (kind::f8f6f4, which reads the codes as
+ * they are): queries enter exactly but for parts below 2^-22 of a head's largest element, and
+ * softmax weights times V scales with 8 (bf16) or 11 (fp16) bits.  Every other call runs on the
+ * CUDA cores in fp32, several times slower.
  *
  *   workspace  device scratch of at least paged_attn_decode_fp4_workspace_size() bytes (may be
  *              NULL when that is 0), 16-byte aligned; it needs no initialisation, and calls

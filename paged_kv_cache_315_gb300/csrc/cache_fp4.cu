@@ -4,8 +4,8 @@
 // nearest to amax / 6 (6 is the largest E2M1 magnitude) and each element's code the E2M1
 // value nearest to x / scale, ties to the even code.  Both kernels are byte movement with a
 // little arithmetic: per element the write reads 2 bytes (16-bit types) and stores half a
-// byte, and at the copy bandwidth of HBM an SM has 7 clocks for 128 of them, some 28 issue
-// slots, so what counts is the number of instructions per element.
+// byte, and at the copy bandwidth of HBM an SM has 14 clocks for 128 of them, that is 14
+// instructions for each element of a lane.
 #include <algorithm>
 #include <type_traits>
 
@@ -144,11 +144,11 @@ __device__ __forceinline__ size_t scale_at(uint32_t slot, int head, int num_head
          (slot - block * static_cast<uint32_t>(block_size));
 }
 
-// One group of D / 16 lanes per (token, head) row, its key and its value row together.  What bounds it
-// is the issue of some 80 instructions per lane and row: with 8 elements a lane instead of 16 the
-// exchanges, the scale and the addresses weigh twice as much (131072 x 8 bf16 rows: 174 us for 134).
-// Four CTAs of one row a lane hide the loads better than fewer with two (2 CTAs: 166 us, 3: 163), and
-// more of them lack registers (6: 157).
+// One group of D / 16 lanes per (token, head) row, its key and its value row together.  131072 x 8
+// bf16 rows take 135 us, 5.0 TB/s, with 67% of the issue slots taken and the loads' latency hidden by
+// other CTAs alone.  With 8 elements a lane instead of 16 the exchanges, the scale and the addresses
+// weigh twice as much: 174 us.  Four CTAs of one row a lane beat fewer of two rows (2 CTAs: 166 us, 3:
+// 163) and more, which lack registers (5: 141, 6: 157).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kWriteCtas)
     write_fp4_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ kc,

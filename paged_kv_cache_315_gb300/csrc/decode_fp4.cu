@@ -269,26 +269,32 @@ __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4
     float m = -INFINITY, l = 0.f;  // of head own_h; l over this lane's tokens alone
     const int32_t* bt = P.block_tables + static_cast<size_t>(seg.s) * P.max_blocks_per_seq;
     for (int tb = seg.t0 + warp * U; tb < seg.t1; tb += kSimtWarps * U) {
-      int id[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) id[u] = tb + u < seg.t1 ? __ldg(&bt[(tb + u) / BS]) : -1;
-      uint32_t kw[U], vw[U];
+      // each lane finds its own token's row and scales; the rows' places go round by shuffles
+      const int t = tb + own_u;
+      const bool live = t < seg.t1;
+      int own_row = -1;  // within the cache (num_blocks * block_size < 2^31), -1: reads as zeros
       float ks = 0.f, vs = 0.f;
+      if (live) {
+        const int j = t / BS, off = t - j * BS;
+        const int id = __ldg(&bt[j]);
+        if (id >= 0 && id < P.num_blocks) {
+          own_row = id * BS + off;
+          const size_t at = (static_cast<size_t>(id) * P.num_kv_heads + g) * BS + off;
+          ks = __bfloat162float(P.k_scales[at]);
+          vs = __bfloat162float(P.v_scales[at]);
+        } else {
+          raise_error(P.err, PKV_DERR_BLOCK_ID);
+        }
+      }
+      uint32_t kw[U], vw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = tb + u, off = t - t / BS * BS;
+        const int row = __shfl_sync(0xffffffffu, own_row, u * G);
         kw[u] = vw[u] = 0;
-        if (id[u] >= 0 && id[u] < P.num_blocks) {
-          const size_t row = (static_cast<size_t>(id[u]) * BS + off) * P.num_kv_heads + g;
-          kw[u] = load_codes<E>(P.k_cache + row * (D / 2), lane);
-          vw[u] = load_codes<E>(P.v_cache + row * (D / 2), lane);
-          if (u == own_u) {
-            const size_t at = (static_cast<size_t>(id[u]) * P.num_kv_heads + g) * BS + off;
-            ks = __bfloat162float(P.k_scales[at]);
-            vs = __bfloat162float(P.v_scales[at]);
-          }
-        } else if (t < seg.t1 && lane == 0) {  // reads as zeros
-          raise_error(P.err, PKV_DERR_BLOCK_ID);
+        if (row >= 0) {
+          const size_t at = (static_cast<size_t>(row) * P.num_kv_heads + g) * (D / 2);
+          kw[u] = load_codes<E>(P.k_cache + at, lane);
+          vw[u] = load_codes<E>(P.v_cache + at, lane);
         }
       }
       float dot[N];
@@ -304,7 +310,6 @@ __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4
           dot[h * U + u] = d;
         }
       }
-      const bool live = tb + own_u < seg.t1;
       const float sum = reduce_heads(dot, [](float x, float y) { return x + y; });
       const float sl = live ? sum * (ks * P.scale_log2) : -INFINITY;
       float mn = sl;

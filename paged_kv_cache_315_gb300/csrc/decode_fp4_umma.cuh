@@ -50,6 +50,14 @@
 // (16 TMA copies of a 16-token block each, at 45-60 clocks from an elected thread in straight-line
 // code, 80 from eight lanes side by side).  The registers follow the roles: 80 a thread at launch,
 // then 88 for softmax warps and 72 for the others.
+//
+// Measured on one GB300 (clocks per tile and SM at 1.92 GHz, 700 being the copy bandwidth): 16
+// contexts of 32k tokens with 1, 2, 4 and 8 query heads for each of 8 KV heads take 806, 814, 826 and
+// 896 with the start and the merge (91 to 101 us); 32 of them with 4 heads 169-173 us, 6.4-6.6 TB/s.
+// Up to 4 heads HBM bounds the steady state.  With 8 the softmax warps' chain does: 2400 clocks a
+// tile in each of the three CTAs, 1600 of them work, with 60% of the issue slots taken.  A call
+// starts with 6 us to the first scores (launch, range, block ids, K), and a sequence of one tile
+// costs a CTA twice what a tile inside a long one does, by its query and its rows.
 
 constexpr int kUTileBytes = kTile * 128;  // a K or V tile in shared memory (64 of 128 bytes data)
 constexpr int kUThreads = 256;
