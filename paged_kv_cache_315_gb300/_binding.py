@@ -528,7 +528,8 @@ def _raw_stream(stream, device: int) -> int:
 
 
 def _scratch(device: int, nbytes: int, workspace, raw: int, stream):
-    """(pointer, bytes) of the caller's workspace or, without one, of the binding's.
+    """The caller's workspace or, without one, the binding's: the tensor, for the caller to hold
+    until the call is made, its pointer and its bytes.
 
     The binding keeps one buffer per (device, stream), like ``workspace_for``, taken from the
     memory of that stream, so that one replaced by a larger one is not handed out while the
@@ -538,7 +539,7 @@ def _scratch(device: int, nbytes: int, workspace, raw: int, stream):
     """
     if workspace is None:
         if nbytes == 0:
-            return None, 0
+            return None, None, 0
         if stream is not None:
             with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
                 return _scratch(device, nbytes, None, raw, None)
@@ -550,9 +551,9 @@ def _scratch(device: int, nbytes: int, workspace, raw: int, stream):
             if workspace is None or workspace.numel() < nbytes:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
                 _workspaces[(device, raw)] = workspace
-        return workspace.data_ptr(), workspace.numel()
+        return workspace, workspace.data_ptr(), workspace.numel()
     _on_current("workspace", (workspace,))
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _fp4_shapes(k_cache, v_cache, k_scales, v_scales):
@@ -651,7 +652,7 @@ def paged_attn_decode_fp4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
     lib = _lib or load()
     MB = table[1]
     raw = _raw_stream(stream, here)
-    ws, ws_bytes = _scratch(
+    held, ws, ws_bytes = _scratch(
         here, lib.paged_attn_decode_fp4_workspace_size(B, Hq, Hkv, D, bs, MB), workspace, raw, stream)
     rc = lib.paged_attn_decode_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -706,8 +707,8 @@ def kv_resize_requests(block_tables: torch.Tensor, context_lens: torch.Tensor,
                        "query_start", tensors)
     lib = _lib or load()
     raw = _raw_stream(stream, here)
-    ws, ws_bytes = _scratch(here, lib.kv_resize_requests_workspace_size(B), workspace, raw,
-                            stream)
+    held, ws, ws_bytes = _scratch(here, lib.kv_resize_requests_workspace_size(B), workspace, raw,
+                                  stream)
     rc = lib.kv_resize_requests(
         block_tables.data_ptr(), context_lens.data_ptr(), target_lens.data_ptr(),
         free_ring.data_ptr(), pool_state.data_ptr(), slot_mapping.data_ptr(), start, B,

@@ -216,9 +216,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // U tokens at a time, whose rows it loads together; their U HN dot products (at most 32) are summed
 // over the lanes by one exchange that leaves each lane with the score of one (token, head), so the
 // softmax of all of them takes one exponential per lane, and the weights go back by broadcasts.
-// The loads in flight bound it (U rows of head_dim / 2 bytes per warp), then the exchanges.
+// The loads in flight bound it (U rows of head_dim / 2 bytes per warp), and with several heads the
+// exchanges.  64 contexts of 1024 to 2048 tokens, 32 query and KV heads: head_dim 64 214 us, with U 16
+// 304 and with 8 404; head_dim 256 325, with U 32, for which registers lack, 432 and with 8 425.
 
-constexpr int simt_tokens(int HN) { return HN == 8 ? 4 : 8; }
+constexpr int simt_tokens(int HN, int E) { return HN == 1 && E >= 4 ? 16 : 32 / HN; }
 
 // A lane's E codes of a row, in the low bits.
 template <int E>
@@ -236,7 +238,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* row, int lane) {
 template <typename T, int E, int HN>
 __global__ void __launch_bounds__(kSimtThreads) decode_fp4_simt_kernel(const Fp4Params P) {
   constexpr int D = 32 * E;
-  constexpr int U = simt_tokens(HN), N = U * HN;
+  constexpr int U = simt_tokens(HN, E), N = U * HN;
   constexpr int G = 32 / N;  // lanes that hold the same (head, token)
   __shared__ float o_s[kSimtWarps][HN][D];
   __shared__ float2 ml_s[kSimtWarps][HN];
