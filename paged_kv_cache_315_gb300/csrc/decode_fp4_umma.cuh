@@ -53,7 +53,7 @@
 //
 // Measured on one GB300 (clocks per tile and SM at 1.92 GHz, 700 being the copy bandwidth): 16
 // contexts of 32k tokens with 1, 2, 4 and 8 query heads for each of 8 KV heads take 806, 814, 826 and
-// 896 with the start and the merge (91 to 101 us); 32 of them with 4 heads 169-173 us, 6.4-6.6 TB/s.
+// 886 with the start and the merge (91 to 99 us); 32 of them with 4 heads 169-173 us, 6.4-6.6 TB/s.
 // Up to 4 heads HBM bounds the steady state.  With 8 the softmax warps' chain does: 2400 clocks a
 // tile in each of the three CTAs, 1600 of them work, with 60% of the issue slots taken.  A call
 // starts with 6 us to the first scores (launch, range, block ids, K), and a sequence of one tile
