@@ -7,7 +7,7 @@
 // and both scales stay outside the products over the codes.
 //
 // Work split.  A sequence of L tokens has ceil(L / 128) tiles.  The tiles of all sequences,
-// in order, are cut into R ranges of equal length (to one tile), and one CTA runs one range
+// in order, are cut into R ranges of equal cost (to one tile), and one CTA runs one range
 // for one (KV head, chunk of query heads) unit; the units of a range are neighbouring CTAs,
 // so the heads of one token, which lie side by side in memory, are read together.  A range
 // may begin inside one sequence and end inside another: a CTA leaves (m, l, o) partials for
@@ -48,16 +48,14 @@ struct Fp4Params {
                     // (or -1), and the last range that holds tiles of it
   unsigned* err;
   int num_seqs, num_q_heads, num_kv_heads, group, chunk, num_chunks;
-  int max_blocks_per_seq, num_blocks, block_size, ranges;
+  int max_blocks_per_seq, num_blocks, block_size, ranges, seq_cost;
   float scale_log2;
 };
 
-// Where a range begins: `tiles` tiles from tile `tile` of sequence `s` on; `total` and
-// `begin` are the tiles of the whole batch and those before the range.  Of P.ranges ranges
-// the first `ranges` hold tiles (one each at least), the others are empty.
+// Where a range begins: `tiles` tiles from tile `tile` of sequence `s` on.  Ranges behind the
+// batch's last tile have none.
 struct Span {
-  int s, tile, tiles, ranges;
-  long long total, begin;
+  int s, tile, tiles;
 };
 
 __device__ __forceinline__ int live_len(const Fp4Params& P, int s) {
@@ -72,7 +70,19 @@ __device__ __forceinline__ long long divide(long long a, int b) {
                         : a / b;
 }
 
-// `total` tiles over `ranges` ranges: the first `extra` of them hold base + 1 tiles each, the
+// The batch lies along a line on which a tile is kTileCost long and each sequence with a context
+// starts with a stretch of P.seq_cost before its second tile, what its query and its rows cost.  The
+// line is cut into equal ranges, and a tile belongs to the range in which it starts.  Cuts lie as far
+// apart as two neighbouring starts at least, so no range is empty.
+//
+// What a sequence costs was measured with 2048 of them, of one tile each: a tile more with 5 to 8
+// query heads in a unit, a sixth of one with fewer.  128 sequences of 128 to 8192 tokens in order of
+// length, 64 query heads over 8 KV heads: 55.8 us (a cost of 0: 56.6, of 7: 56.1).
+constexpr int kTileCost = 4;
+constexpr int kSeqCostMany = 4;
+constexpr int kSeqCostFew = 1;
+
+// A line of length `total` in `ranges` pieces: the first `extra` of them are base + 1 long, the
 // others base.
 struct Cut {
   long long base;
@@ -82,7 +92,7 @@ struct Cut {
     extra = static_cast<int>(total - base * ranges);
   }
   __device__ __forceinline__ long long begin(int r) const { return base * r + min(r, extra); }
-  // The range that holds tile x.
+  // The range that holds point x.
   __device__ __forceinline__ int of(long long x) const {
     const long long big = (base + 1) * extra;
     return static_cast<int>(x < big ? x / (base + 1) : extra + (x - big) / base);
@@ -98,67 +108,112 @@ constexpr int kLens = 64;
 template <int THREADS>
 __device__ Span find_span(const Fp4Params& P, int r, bool notes, int* lens) {
   constexpr int W = THREADS / 32;
-  __shared__ long long warp_tot[W];
+  __shared__ long long warp_tiles[W];
+  __shared__ int warp_seqs[W];
   __shared__ int found_s, found_tile;
-  __shared__ int2 cut;
+  __shared__ long long found[2];  // the batch's tiles before the range's begin and before its end
+  __shared__ int2 past;           // the sequence that the range's end cuts (or -1), and its last range
+  __shared__ long long past_first;  // and the batch's tiles before it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = P.max_blocks_per_seq * P.block_size;
   const int per = (P.num_seqs + THREADS - 1) / THREADS;
   const int s0 = min(P.num_seqs, tid * per), s1 = min(P.num_seqs, s0 + per);
   long long own = 0;
+  int own_seqs = 0;
   for (int s = s0; s < s1; ++s) {
     const int L = P.context_lens[s];
     if (notes && r == 0 && (L < 0 || L > cap)) raise_error(P.err, PKV_DERR_CONTEXT);
     own += (min(max(L, 0), cap) + kTile - 1) / kTile;
+    own_seqs += min(L, cap) > 0;
   }
   long long incl = own;
+  int seqs = own_seqs;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int z = __shfl_up_sync(0xffffffffu, seqs, o);
+    if (lane >= o) {
+      incl += y;
+      seqs += z;
+    }
   }
-  if (lane == 31) warp_tot[warp] = incl;
-  if (tid == 0) cut = make_int2(-1, 0);
+  if (lane == 31) {
+    warp_tiles[warp] = incl;
+    warp_seqs[warp] = seqs;
+  }
+  if (tid == 0) past = make_int2(-1, 0);
   __syncthreads();
-  long long before = 0, total = 0;
+  long long before = incl - own, total = 0;
+  int before_seqs = seqs - own_seqs, total_seqs = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    if (w < warp) before += warp_tot[w];
-    total += warp_tot[w];
+    if (w < warp) {
+      before += warp_tiles[w];
+      before_seqs += warp_seqs[w];
+    }
+    total += warp_tiles[w];
+    total_seqs += warp_seqs[w];
   }
-  Span sp;
-  sp.total = total;
-  sp.ranges = static_cast<int>(min(static_cast<long long>(P.ranges), total));
-  const Cut ranges(total, sp.ranges);
-  sp.begin = r < sp.ranges ? ranges.begin(r) : total;
-  sp.tiles = r < sp.ranges ? static_cast<int>(ranges.begin(r + 1) - sp.begin) : 0;
-  const long long at = before + incl - own, end = sp.begin + sp.tiles;
-  // the sequence that holds tile `x`, one of this thread's, and the first tile of it
-  auto holder = [&](long long x, long long& first, int& tiles) {
-    int s = s0;
-    for (first = at;; ++s) {  // one of them holds it
+  // (few tiles: as many ranges as can be, whatever they cost)
+  const int cost = total >= 4LL * P.ranges ? P.seq_cost : 0;
+  const long long line = total * kTileCost + static_cast<long long>(total_seqs) * cost;
+  const int ranges = static_cast<int>(min(static_cast<long long>(P.ranges), total));
+  const Cut cuts(line, ranges);
+  const long long begin = r < ranges ? cuts.begin(r) : line;
+  const long long end = r < ranges ? cuts.begin(r + 1) : line;
+  const long long at = before * kTileCost + static_cast<long long>(before_seqs) * cost;
+  const long long own_end = at + own * kTileCost + static_cast<long long>(own_seqs) * cost;
+  // The first tile that starts at point x or behind it, x lying in sequence s of this thread, whose
+  // `tiles` tiles begin with the batch's tile `first`: its number in the sequence, or `tiles` (then it
+  // is the next sequence's first).  `last` is where the sequence's last tile starts.
+  auto tile_at = [&](long long x, int& s, long long& first, int& tiles, long long& last) {
+    long long start = at;
+    first = before;
+    for (s = s0;; ++s) {  // one of them holds it
       tiles = (live_len(P, s) + kTile - 1) / kTile;
-      if (x < first + tiles) return s;
+      const long long length = tiles > 0 ? static_cast<long long>(tiles) * kTileCost + cost : 0;
+      if (x < start + length) break;
+      start += length;
       first += tiles;
     }
+    last = tiles > 1 ? start + cost + static_cast<long long>(tiles - 1) * kTileCost : start;
+    if (x == start) return 0;
+    const long long in = x - start - cost;
+    return in <= kTileCost ? 1 : static_cast<int>((in + kTileCost - 1) / kTileCost);
   };
-  long long first;
-  int tiles;
-  if (at <= sp.begin && sp.begin < at + own) {
-    found_s = holder(sp.begin, first, tiles);
-    found_tile = static_cast<int>(sp.begin - first);
+  int s, tiles;
+  long long first, last;
+  if (at <= begin && begin < own_end) {
+    int tile = tile_at(begin, s, first, tiles, last);
+    found[0] = first + tile;
+    if (tile >= tiles) {  // r < ranges: a tile starts in the range, so a sequence with tiles follows
+      tile = 0;
+      do ++s;
+      while (live_len(P, s) == 0);
+    }
+    found_s = s;
+    found_tile = tile;
   }
-  if (notes && sp.tiles > 0 && at < end && end < at + own) {
-    const int s = holder(end, first, tiles);
-    if (first >= sp.begin && first < end)  // begins in the range and goes on past it
-      cut = make_int2(s, ranges.of(first + tiles - 1));
+  if (at <= end && end < own_end) {
+    const int tile = tile_at(end, s, first, tiles, last);
+    found[1] = first + tile;
+    if (notes && tile > 0 && tile < tiles) {
+      past = make_int2(s, cuts.of(last));
+      past_first = first;
+    }
+  } else if (tid == 0 && end >= line) {
+    found[1] = total;
   }
   __syncthreads();
-  if (notes && tid == 0 && P.ranges > 1) P.info[r] = cut;
+  Span sp;
+  sp.tiles = r < ranges ? static_cast<int>(found[1] - found[0]) : 0;
   sp.s = sp.tiles > 0 ? found_s : 0;
   sp.tile = sp.tiles > 0 ? found_tile : 0;
+  // (a sequence that begins before the range is noted by the range it begins in)
+  if (notes && tid == 0 && P.ranges > 1)
+    P.info[r] = sp.tiles > 0 && past.x >= 0 && past_first >= found[0] ? past : make_int2(-1, 0);
   if (lens != nullptr) {
-    for (int s = max(s0, sp.s); s < min(s1, sp.s + kLens); ++s) lens[s - sp.s] = live_len(P, s);
+    for (int i = max(s0, sp.s); i < min(s1, sp.s + kLens); ++i) lens[i - sp.s] = live_len(P, i);
     __syncthreads();
   }
   return sp;
@@ -688,6 +743,7 @@ int launch_decode_fp4(const DecodeFp4Args& a, cudaStream_t stream) {
   P.ranges = umma && a.dtype == PKV_F16 && w.chunk > 4
                  ? std::max(1, std::min(w.ranges, kRangeCtas * 2 / 3 / (a.num_kv_heads * w.num_chunks)))
                  : w.ranges;
+  P.seq_cost = umma && w.chunk > 4 ? kSeqCostMany : kSeqCostFew;
   P.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const long long grid = static_cast<long long>(P.ranges) * a.num_kv_heads * w.num_chunks;
   if (grid > INT_MAX || (P.ranges > 1 && a.num_q_heads > 65535)) return PKV_EUNSUPPORTED;
