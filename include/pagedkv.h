@@ -375,9 +375,9 @@ int kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache
  * never used, a live block id out of range sets PKV_DERR_BLOCK_ID and reads as zeros, a
  * context length outside the table sets PKV_DERR_CONTEXT and is clamped.
  *
- * The contexts' 128-token tiles are cut into ranges of equal cost, one CTA for each range and KV head
- * (and chunk of at most 8 query heads), whatever the lengths of the sequences; a sequence cut
- * by a range's end is merged by log-sum-exp in a second grid.  The result does not depend on
+ * The contexts' 128-token tiles are cut into ranges of equal cost, one CTA for each range and
+ * KV head (and chunk of at most 8 query heads), whatever the lengths of the sequences; a
+ * sequence cut by a range's end is merged by log-sum-exp in a second grid.  The result does not depend on
  * how the work happened to be scheduled: equal inputs give equal outputs.
  *
  * With head_dim 128, block_size 8, 16, 32, 64 or 128, q and out in 16 bits and scales aligned

@@ -417,6 +417,22 @@ def test_decode_more_tiles_than_ranges(pkv, dtype, Hq, Hkv, D, bs):
     c.check(got)
 
 
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling"])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [("bf16", 40, 40, 128), ("bf16", 96, 16, 128),
+                                            ("f16", 64, 8, 128), ("bf16", 16, 16, 64),
+                                            ("f32", 32, 16, 32)])
+def test_decode_ranges_of_many_short_sequences(pkv, dtype, Hq, Hkv, D, order):
+    """More than four tiles to a range, where a sequence's start counts beside its tiles."""
+    lens = np.arange(240) * 37 % 450
+    lens[::17] = 0
+    if order != "mixed":
+        lens = np.sort(lens)[::1 if order == "rising" else -1].copy()
+    c = Case(dtype, Hq, Hkv, D, 16, lens, seed=D + Hq)
+    got = c.run(pkv)
+    assert pkv.pkv_device_error() == 0
+    c.check(got)
+
+
 # ---- together ---------------------------------------------------------------------------------
 
 
